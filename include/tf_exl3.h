@@ -54,7 +54,9 @@ enum {
   TF_E_ALIGN = -6,  /* trellis or z not 16-byte aligned, or a row buffer not element-aligned */
   TF_E_ALIAS = -7,  /* an output overlaps an input */
   TF_E_WAVES = -8,  /* waves not in {0, 4, 8} */
-  TF_E_LAUNCH = -9  /* the HIP runtime reported an error at launch */
+  TF_E_LAUNCH = -9, /* the HIP runtime reported an error at launch */
+  TF_E_SIZE = -10,  /* a size, stride or scale of an operator around the projection is out of its range */
+  TF_E_WORKSPACE = -11 /* the workspace is smaller than the call needs */
 };
 
 /*
@@ -279,6 +281,169 @@ int tf_exl3_debug_linear_mfma_split(int bits, int rows, int in_dim, int out_dim,
  */
 int tf_exl3_calib_copy(const void* src, void* dst, size_t bytes, int blocks, void* stream);
 int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int blocks, void* stream);
+
+/*
+ * Operators around the projection: attention of a tree of drafted tokens over a
+ * paged cache, the cache's append, the verification of the drafts against the
+ * head's logits, and the distillation loss that trains a drafter on a teacher's
+ * top logits. No page defines them; each formula is stated here.
+ *
+ * Strides are in elements. Innermost dimensions are contiguous (stride 1). What
+ * lives on the device (lengths, page numbers, masks, node numbers, parents,
+ * tokens) cannot be refused on the host: every kernel bounds it before an
+ * address is made of it, as stated at each call. A workspace belongs to one call
+ * at a time, needs no initial contents and may be used again, or freed in
+ * stream order, after the call.
+ */
+
+/*
+ * tree_attention: nodes of a drafted tree attend to their sequence's cache and,
+ * by a mask, to each other.
+ *
+ *   x[j] = scale * sum_d q[b][i][h][d] * K[j][g][d],   g = h / (q_heads / kv_heads)
+ *   out[b][i][h] = cast( sum_j exp(x[j] - max x) V[j][g] / sum_j exp(x[j] - max x) )
+ *
+ * over the keys j that node i of sequence b sees: cache positions 0 .. lengths[b] - 1,
+ * all of them, and the tree's node t (k[b][t], v[b][t]) where bit t of mask[b][i]
+ * is set. A node that sees no key gets zeros. Products of the 16-bit inputs are
+ * summed in fp32; probabilities are rounded to the inputs' type for the second
+ * product (half an ulp each, unbiased), their sum and the output stay in fp32
+ * until the one rounding of the output. A value that no node may see never
+ * reaches an output, infinities and NaN included.
+ *
+ * Position p of sequence b is slot p % page_size of page table[b][p / page_size].
+ * lengths[b] is taken as 0 below 0 and as table_pages * page_size above that; a
+ * page number outside [0, pages) is read as page 0 (in range, meaningless values).
+ *
+ *   dtype      TF_DT_F16 or TF_DT_BF16 (q, k, v, both caches and out)
+ *   head_dim   a multiple of 16, up to 256
+ *   nodes      1 .. 64; q_heads a multiple of kv_heads
+ *   strides    of q, k, v, out: [batch, node, head]; of the caches: [page, slot, head];
+ *              multiples of 8 elements, pointers 16-byte aligned (out: 4 elements, 8 bytes)
+ *   workspace  tf_exl3_tree_attention_workspace(a) bytes, 16-byte aligned
+ */
+typedef struct tf_exl3_tree_attention_args {
+  int dtype, batch, nodes, q_heads, kv_heads, head_dim;
+  int pages, page_size, table_pages;
+  float scale;
+  const void *q, *k, *v;
+  const int64_t* mask;       /* [batch][nodes] */
+  const void *k_cache, *v_cache;
+  const int32_t* table;      /* [batch][table_pages], rows table_stride apart */
+  const int32_t* lengths;    /* [batch] */
+  void* out;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t q_stride[3], k_stride[3], v_stride[3], k_cache_stride[3], v_cache_stride[3], out_stride[3];
+  int64_t table_stride;
+} tf_exl3_tree_attention_args;
+
+int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* a, void* stream);
+
+/* Bytes of workspace a call of these sizes needs (0 where the sizes are refused).
+ * Reads dtype, batch, nodes, heads, head_dim, page_size and table_pages only. */
+size_t tf_exl3_tree_attention_workspace(const tf_exl3_tree_attention_args* a);
+
+/*
+ * cache_append: rows of k and v into the cache's pages, byte for byte.
+ *
+ *   position lengths[b] + j of sequence b <- k[b][t], v[b][t],  t = nodes[b][j] (nodes
+ *   NULL: t = j), for j < counts[b] (counts NULL: all of them)
+ *
+ * counts[b] is taken within [0, tokens]. Nothing is written for a t outside
+ * [0, tokens), a position outside the table or a page number outside [0, pages);
+ * lengths stays as it is. Two rows of one call that go to the same slot leave
+ * either of them there.
+ *
+ *   elem_bytes  bytes of an element: 1, 2 or 4
+ *   strides     as in tree_attention, any alignment of whole elements
+ */
+typedef struct tf_exl3_cache_append_args {
+  int elem_bytes, batch, tokens, kv_heads, head_dim;
+  int pages, page_size, table_pages;
+  const void *k, *v;
+  void *k_cache, *v_cache;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* nodes;   /* [batch][tokens] or NULL */
+  const int32_t* counts;  /* [batch] or NULL */
+  int64_t k_stride[3], v_stride[3], k_cache_stride[3], v_cache_stride[3];
+  int64_t table_stride;
+} tf_exl3_cache_append_args;
+
+int tf_exl3_cache_append(const tf_exl3_cache_append_args* a, void* stream);
+
+/*
+ * Weights of a row of logits x at temperature T > 0: w[i] = exp((x[i] - max x) / T) in
+ * 64 bits; at T <= 0 one weight of 1 at the first place of the maximum; a NULL
+ * temperature is T = 1 for every sequence. A logit of -inf or NaN has no weight; where
+ * +inf occurs, its places alone have weight. The token of a row for u in [0, 1) is the
+ * first place whose running sum of weights is over u times their sum (neither rounding
+ * nor a u of 1 or more goes past the last place that has weight; a u below 0 or NaN
+ * counts as 0). A row without any weight has the token -1.
+ *
+ * verify_tree: walks each sequence's tree of drafted tokens down the tokens that the
+ * target's rows choose. t[i] = token of logits[b][i] for u[b][i]. The walk begins at node
+ * 0 (the last token before the drafts); at node i it goes on to the first node c > i with
+ * parents[b][c] == i and tokens[b][c] == t[i], and ends where there is none.
+ *
+ *   accepted [batch][nodes]: the walk's nodes in order, then -1
+ *   count    [batch]: how many
+ *   next     [batch]: t of the walk's last node
+ *
+ *   logits [batch][nodes][vocab], strides of batch and node; tokens, parents int32
+ *   [batch][nodes]; u fp32 [batch][nodes]; temperature fp32 [batch] or NULL
+ *
+ * verify_chain: speculative sampling of a chain. Draft j (tokens[b][j + 1], drawn from
+ * q[b][j]) is accepted while u[b][j] * q[b][j][x] < p[b][j][x], p = w / sum w of
+ * logits[b][j]; j = 0 .. nodes - 2 in turn. tokens[b][0] is not read. A draft outside
+ * the vocabulary is refused.
+ *
+ *   count [batch]: 1 + accepted drafts
+ *   next  [batch]: with a = count - 1: the token, for u[b][nodes - 1], of the weights
+ *         max(p[b][a] - q[b][a], 0) in place of w where a draft was refused (of p[b][a] where
+ *         they are all 0), of p[b][a] where none was
+ *
+ *   q fp32 [batch][nodes - 1][vocab], strides of batch and node
+ *
+ * Limits: nodes 1 .. 1024, vocab below 2^31. workspace: the call's *_workspace bytes,
+ * 16-byte aligned.
+ */
+int tf_exl3_verify_tree(int dtype, int batch, int nodes, int vocab, const void* logits, int64_t stride_batch,
+                        int64_t stride_node, const int32_t* tokens, const int32_t* parents, const float* u,
+                        const float* temperature, int32_t* accepted, int32_t* count, int32_t* next,
+                        void* workspace, size_t workspace_bytes, void* stream);
+int tf_exl3_verify_chain(int dtype, int batch, int nodes, int vocab, const void* logits, int64_t stride_batch,
+                         int64_t stride_node, const int32_t* tokens, const float* q, int64_t q_stride_batch,
+                         int64_t q_stride_node, const float* u, const float* temperature, int32_t* count,
+                         int32_t* next, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace for either call (0 where the sizes are refused). */
+size_t tf_exl3_verify_workspace(int batch, int nodes, int vocab);
+
+/*
+ * distill: the loss of rows of logits x against a teacher's top logits y at places
+ * index, and its gradient.
+ *
+ *   t = softmax(y / T) over the entries with index in [0, vocab), others left out
+ *   p = softmax(x / T)
+ *   loss[r] = sum over entries of t (ln t - ln p[index]), terms with t = 0 left out
+ *   grad[r][i] = cast( weight[r] / T * (p[i] - sum of the t whose index is i) )
+ *
+ * grad is that of sum_r weight[r] * loss[r] by x. A row without entries, or of weight 0,
+ * has a gradient of 0, the former a loss of 0. An index may occur more than once. Sums,
+ * maxima and the logarithm are in fp32.
+ *
+ *   loss     fp32 [rows] or NULL;  grad [rows][vocab] of the logits' type or NULL
+ *   logits   [rows][vocab], rows logits_stride apart; rows may begin at any element
+ *   index    int32 [rows][top_k], top of type top_dtype [rows][top_k], top_k 1 .. 1024
+ *   weight   fp32 [rows] (needed for grad)
+ *   workspace tf_exl3_distill_workspace bytes, 16-byte aligned
+ */
+int tf_exl3_distill(int dtype, int rows, int vocab, int top_k, const void* logits, int64_t logits_stride,
+                    const int32_t* index, const void* top, int top_dtype, const float* weight, float temperature,
+                    float* loss, void* grad, int64_t grad_stride, void* workspace, size_t workspace_bytes,
+                    void* stream);
+size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,6 @@
-"""EXL3 decode-row projection for MI355X (gfx950): rot_in and the trellis linear.
+"""EXL3 decode-row projection for MI355X (gfx950): rot_in and the trellis linear, and
+the operators around it: attention of drafted trees over a paged cache, the cache's
+append, verification of the drafts and distillation of a drafter.
 
 The compute runs in libtf_exl3.so (hand-written HIP kernels behind the C ABI in
 include/tf_exl3.h); this package only marshals torch tensors and streams into
@@ -27,6 +29,15 @@ from ._lib import (  # noqa: F401
     rot_in,
     status_string,
     trellis_bytes,
+)
+from ._ops import (  # noqa: F401
+    cache_append,
+    distill,
+    distill_grad,
+    distill_loss,
+    tree_attention,
+    verify_chain,
+    verify_tree,
 )
 
 WIDTHS = (2, 3, 4, 5, 6, 8)

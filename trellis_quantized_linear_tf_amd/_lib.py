@@ -21,6 +21,7 @@ TF_OK = 0
 STATUS = {
     0: "TF_OK", -1: "TF_E_BITS", -2: "TF_E_SHAPE", -3: "TF_E_ROWS", -4: "TF_E_DTYPE",
     -5: "TF_E_NULL", -6: "TF_E_ALIGN", -7: "TF_E_ALIAS", -8: "TF_E_WAVES", -9: "TF_E_LAUNCH",
+    -10: "TF_E_SIZE", -11: "TF_E_WORKSPACE",
 }
 
 
@@ -49,6 +50,33 @@ class Plan(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_Z = ctypes.c_size_t
+_F = ctypes.c_float
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        *((n, _I) for n in ("dtype", "batch", "nodes", "q_heads", "kv_heads", "head_dim", "pages", "page_size",
+                            "table_pages")),
+        ("scale", _F),
+        *((n, _P) for n in ("q", "k", "v", "mask", "k_cache", "v_cache", "table", "lengths", "out", "workspace")),
+        ("workspace_bytes", _Z),
+        *((n, _L * 3) for n in ("q_stride", "k_stride", "v_stride", "k_cache_stride", "v_cache_stride", "out_stride")),
+        ("table_stride", _L),
+    ]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    _fields_ = [
+        *((n, _I) for n in ("elem_bytes", "batch", "tokens", "kv_heads", "head_dim", "pages", "page_size",
+                            "table_pages")),
+        *((n, _P) for n in ("k", "v", "k_cache", "v_cache", "table", "lengths", "nodes", "counts")),
+        *((n, _L * 3) for n in ("k_stride", "v_stride", "k_cache_stride", "v_cache_stride")),
+        ("table_stride", _L),
+    ]
+
+
 SIGNATURES = {
     "tf_exl3_rot_in": (_I, [_P, _I, _P, _P, _I, _I, _P]),
     "tf_exl3_linear": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P]),
@@ -65,6 +93,14 @@ SIGNATURES = {
     "tf_exl3_status_string": (ctypes.c_char_p, [_I]),
     "tf_exl3_debug_decode_states": (_I, [_P, _P, _I, _P]),
     "tf_exl3_debug_decode_tiles": (_I, [_I, _I, _I, _P, _P, _P]),
+    "tf_exl3_tree_attention": (_I, [ctypes.POINTER(TreeAttentionArgs), _P]),
+    "tf_exl3_tree_attention_workspace": (_Z, [ctypes.POINTER(TreeAttentionArgs)]),
+    "tf_exl3_cache_append": (_I, [ctypes.POINTER(CacheAppendArgs), _P]),
+    "tf_exl3_verify_tree": (_I, [_I, _I, _I, _I, _P, _L, _L, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "tf_exl3_verify_chain": (_I, [_I, _I, _I, _I, _P, _L, _L, _P, _P, _L, _L, _P, _P, _P, _P, _P, _Z, _P]),
+    "tf_exl3_verify_workspace": (_Z, [_I, _I, _I]),
+    "tf_exl3_distill": (_I, [_I, _I, _I, _I, _P, _L, _P, _P, _I, _P, _F, _P, _P, _L, _P, _Z, _P]),
+    "tf_exl3_distill_workspace": (_Z, [_I, _I, _I, _I]),
     "tf_exl3_calib_copy": (_I, [_P, _P, ctypes.c_size_t, _I, _P]),
     "tf_exl3_calib_stream_read": (_I, [_P, ctypes.c_size_t, _P, _I, _P]),
 }

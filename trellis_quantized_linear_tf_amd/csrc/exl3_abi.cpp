@@ -79,6 +79,8 @@ const char* tf_exl3_status_string(int status) {
     case TF_E_ALIAS: return "an output buffer overlaps an input buffer";
     case TF_E_WAVES: return "waves must be 0 (auto), 4 or 8";
     case TF_E_LAUNCH: return "the HIP runtime reported an error at launch";
+    case TF_E_SIZE: return "a size, stride or scale is out of the operator's range";
+    case TF_E_WORKSPACE: return "the workspace is smaller than the call needs";
     default: return "unknown status";
   }
 }
