@@ -1,5 +1,5 @@
-// Device helpers of the operators around the projection: element types, wave and
-// workgroup reductions in a fixed order.
+// Device helpers of the operators around the projection: element types, 16-byte pieces
+// of rows, wave and workgroup reductions in a fixed order.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -9,26 +9,91 @@
 
 namespace tf_exl3 {
 
-// Element of a row of type DT as fp32 (exact for all three types).
+// 16 bytes of a row, at any alignment of whole elements: gfx950 loads and stores
+// unaligned vectors whole, and the cache lines that two pieces share come from L1.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_elem __attribute__((aligned(2)));
+
+__device__ __forceinline__ u32x4 load_piece(const void* p) { return *static_cast<const u32x4_elem*>(p); }
+__device__ __forceinline__ void store_piece(void* p, u32x4 v) { *static_cast<u32x4_elem*>(p) = v; }
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Elements of a row of type DT as fp32 (exact for all three types), single and by the
+// piece; fp32 -> DT rounds to nearest even.
 template <int DT>
 struct Elem;
+
 template <>
 struct Elem<TF_DT_F32> {
   typedef float type;
+  static constexpr int kPiece = 4;
+  static constexpr uint32_t kMinusInf = 0xFF800000u;  // a piece's dword of -inf
   __device__ static float load(float v) { return v; }
   __device__ static float store(float v) { return v; }
+  __device__ static void unpack(u32x4 v, float (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = bits_to_f32(v[i]);
+  }
+  __device__ static u32x4 pack(const float (&x)[4]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f32_to_bits(x[i]);
+    return v;
+  }
 };
+
 template <>
 struct Elem<TF_DT_F16> {
   typedef uint16_t type;
+  static constexpr int kPiece = 8;
+  static constexpr uint32_t kMinusInf = 0xFC00FC00u;
   __device__ static float load(uint16_t v) { return f16_bits_to_f32(v); }
   __device__ static uint16_t store(float v) { return f32_to_f16_bits(v); }
+  __device__ static void unpack(u32x4 v, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = v[i];  // a bit_cast of the element itself takes element 0
+      const half2_t h = __builtin_bit_cast(half2_t, u);
+      x[2 * i] = (float)h[0];
+      x[2 * i + 1] = (float)h[1];
+    }
+  }
+  __device__ static u32x4 pack(const float (&x)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const half2_t h = {(_Float16)x[2 * i], (_Float16)x[2 * i + 1]};
+      v[i] = __builtin_bit_cast(uint32_t, h);
+    }
+    return v;
+  }
 };
+
 template <>
 struct Elem<TF_DT_BF16> {
   typedef uint16_t type;
+  static constexpr int kPiece = 8;
+  static constexpr uint32_t kMinusInf = 0xFF80FF80u;
   __device__ static float load(uint16_t v) { return bf16_bits_to_f32(v); }
   __device__ static uint16_t store(float v) { return f32_to_bf16_bits(v); }
+  __device__ static void unpack(u32x4 v, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bits_to_f32(v[i] << 16);
+      x[2 * i + 1] = bits_to_f32(v[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static u32x4 pack(const float (&x)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 f = {x[2 * i], x[2 * i + 1]};
+      v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+    }
+    return v;
+  }
 };
 
 __device__ __forceinline__ float load_elem(const void* p, int dtype, int64_t i) {
