@@ -102,6 +102,20 @@ __device__ __forceinline__ float load_elem(const void* p, int dtype, int64_t i) 
   return dtype == TF_DT_F16 ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
 }
 
+// n / d for 0 <= n < 2^31 by a product: with 2^s >= d, m = ceil(2^(31 + s) / d) exceeds the
+// true factor by less than 2^s / 2^(31 + s) of n's range, so the quotient is exact.
+struct FastDiv {
+  uint32_t m;
+  int shift;
+  __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+
+inline FastDiv fast_div(int d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  return {(uint32_t)(((1ull << (31 + s)) + (uint64_t)d - 1) / (uint64_t)d), 31 + s};
+}
+
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
