@@ -1,4 +1,23 @@
 // Attention of a tree of drafted tokens over a paged cache.
+//
+// The rows of one kv head, (node, query head of its group), share every key. A workgroup
+// takes a run of a sequence's positions (the cache's, then the nodes') for up to
+// 16 RT RG of those rows, and walks it in tiles of KG KW positions that all its waves
+// load together: keys and values go through registers, a tile ahead, into shared memory.
+// Of its waves, RG groups share the rows and KG groups a tile's positions.
+//
+// Products are taken transposed, on 16x16x32 matrix instructions: S^T = K Q^T leaves a
+// lane with 4 positions of one row per tile of 16, so the row's maximum is a maximum over
+// registers and two lane swaps, its sum stays a lane's own to the end, and the
+// probabilities are already where O^T = V^T P^T wants them: with the 32 positions of a
+// step taken in the order {4g .. 4g+3, 16+4g .. 16+4g+3} for lane group g, in which V^T is
+// read from shared memory by the transposing loads. Scores, statistics and outputs are
+// in fp32; probabilities are rounded to the inputs' type for the second product (half a
+// unit in the last place each, which the sum of fp32 probabilities does not see).
+//
+// Positions are split over workgroups so that the chip is full whatever the lengths are:
+// every workgroup finds its run from the lengths on the device. Runs leave fp32 outputs
+// with their maximum and sum, and a second kernel joins them.
 #include <math.h>
 
 #include "ops_device.hpp"
@@ -6,66 +25,615 @@
 
 namespace tf_exl3 {
 
-// One wave per (head, node, sequence). Lane l holds dimensions l, l + 64, ... of the
-// query and of the running output; keys come one at a time, with the running maximum
-// and sum of the softmax.
-template <int DT>
-__global__ __launch_bounds__(64) void tree_attention_kernel(tf_exl3_tree_attention_args a) {
-  typedef typename Elem<DT>::type T;
-  const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z, lane = threadIdx.x;
-  const int g = h / (a.q_heads / a.kv_heads);
-  const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0] + i * a.q_stride[1] + h * a.q_stride[2];
-  float qr[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) qr[c] = c * 64 + lane < a.head_dim ? Elem<DT>::load(q[c * 64 + lane]) : 0.f;
-  const int64_t room = (int64_t)a.table_pages * a.page_size;
-  int64_t len = a.lengths[b];
-  len = len < 0 ? 0 : len > room ? room : len;
-  const uint64_t seen = (uint64_t)a.mask[(int64_t)b * a.nodes + i];
-  float m = -INFINITY, z = 0.f;
-  for (int64_t j = 0; j < len + a.nodes; ++j) {
-    const T *k, *v;
-    if (j < len) {
-      int page = a.table[b * a.table_stride + j / a.page_size];
-      if (page < 0 || page >= a.pages) page = 0;
-      const int64_t slot = j % a.page_size;
-      k = static_cast<const T*>(a.k_cache) + page * a.k_cache_stride[0] + slot * a.k_cache_stride[1] +
-          g * a.k_cache_stride[2];
-      v = static_cast<const T*>(a.v_cache) + page * a.v_cache_stride[0] + slot * a.v_cache_stride[1] +
-          g * a.v_cache_stride[2];
-    } else {
-      const int t = (int)(j - len);
-      if (!((seen >> t) & 1)) continue;
-      k = static_cast<const T*>(a.k) + b * a.k_stride[0] + t * a.k_stride[1] + g * a.k_stride[2];
-      v = static_cast<const T*>(a.v) + b * a.v_stride[0] + t * a.v_stride[1] + g * a.v_stride[2];
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c * 64 + lane < a.head_dim) x = __builtin_fmaf(qr[c], Elem<DT>::load(k[c * 64 + lane]), x);
-    x = wave_sum(x) * a.scale;
-    const float top = fmaxf(m, x);
-    const float keep = m == -INFINITY ? 0.f : expf(m - top), p = expf(x - top);
-    z = z * keep + p;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c * 64 + lane < a.head_dim) o[c] = __builtin_fmaf(p, Elem<DT>::load(v[c * 64 + lane]), o[c] * keep);
-    m = top;
-  }
-  T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + i * a.out_stride[1] + h * a.out_stride[2];
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (c * 64 + lane < a.head_dim) out[c * 64 + lane] = Elem<DT>::store(z == 0.f ? 0.f : o[c] / z);
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+struct AttnPlan {
+  int rows, group;      // of one kv head: nodes * group
+  int row_tiles;        // workgroups that share a run's positions
+  int units;            // runs, at most
+  int target;           // runs to aim for over all sequences; 0: one each
+  int min_tiles;        // of a run
+  float c;              // |scale| log2(e)
+  bool negate;          // scale < 0
+  FastDiv by_group, by_page, by_row_tiles, by_heads, by_quads;
+  int2* seq;            // [batch] first run, runs
+  float2* stat;         // [unit][head][row] maximum (in log2 units), sum
+  float* part;          // [unit][head][row][dim]
+};
+
+// The kernel's arguments, read from the argument segment where they are needed: the
+// asm keeps each phase's reads in that phase, or all of them would live in scalar
+// registers (and spill) from the start.
+struct AttnArgs {
+  tf_exl3_tree_attention_args a;
+  AttnPlan p;
+};
+typedef const __attribute__((address_space(4))) AttnArgs* ArgPtr;
+typedef const __attribute__((address_space(4))) FastDiv* DivPtr;
+
+__device__ __forceinline__ ArgPtr arguments() {
+  ArgPtr x = (ArgPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(x));
+  return x;
 }
 
-size_t tree_attention_workspace(const tf_exl3_tree_attention_args&) { return 16; }
+__device__ __forceinline__ FastDiv copy(DivPtr d) { return {d->m, d->shift}; }
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == TF_DT_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (DT == TF_DT_F16) {
+    const half2_t h = {(_Float16)lo, (_Float16)hi};
+    return __builtin_bit_cast(uint32_t, h);
+  } else {
+    const f32x2 f = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+  }
+}
+
+// The four lane groups' values of a row (lanes l, l + 16, l + 32, l + 48), joined.
+__device__ __forceinline__ float groups_max(float v) {
+  u32x2 s = __builtin_amdgcn_permlane16_swap(f32_to_bits(v), f32_to_bits(v), false, false);
+  v = fmaxf(bits_to_f32(s[0]), bits_to_f32(s[1]));
+  s = __builtin_amdgcn_permlane32_swap(f32_to_bits(v), f32_to_bits(v), false, false);
+  return fmaxf(bits_to_f32(s[0]), bits_to_f32(s[1]));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+  u32x2 s = __builtin_amdgcn_permlane16_swap(f32_to_bits(v), f32_to_bits(v), false, false);
+  v = bits_to_f32(s[0]) + bits_to_f32(s[1]);
+  s = __builtin_amdgcn_permlane32_swap(f32_to_bits(v), f32_to_bits(v), false, false);
+  return bits_to_f32(s[0]) + bits_to_f32(s[1]);
+}
+
+__device__ __forceinline__ int cached(ArgPtr x, int b) {
+  const int64_t room = (int64_t)x->a.table_pages * x->a.page_size;
+  const int64_t len = x->a.lengths[b];
+  return (int)(len < 0 ? 0 : len > room ? room : len);
+}
+
+struct Run {
+  int b, first, runs;  // sequence, its first run, its runs
+  int begin, end;      // in tiles
+};
+
+// Run `unit` of the batch: a sequence of t tiles is cut into ceil(t / P) runs of equal size,
+// P = max(min_tiles, ceil(all tiles / target)), so there are at most target + batch.
+template <int KT>
+__device__ __forceinline__ bool find_run(ArgPtr x, int unit, Run* r) {
+  const int batch = x->a.batch, nodes = x->a.nodes, target = x->p.target;
+  if (target == 0) {
+    r->b = unit, r->first = unit, r->runs = 1, r->begin = 0;
+    r->end = (cached(x, unit) + nodes + KT - 1) / KT;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t all = 0;
+  for (int b = lane; b < batch; b += 64) all += (cached(x, b) + nodes + KT - 1) / KT;
+  all = wave_sum(all);
+  const int64_t aim = (all + target - 1) / target;
+  const int size = (int)(aim < x->p.min_tiles ? x->p.min_tiles : aim);
+  int base = 0;
+  for (int b0 = 0; b0 < batch; b0 += 64) {
+    const int tiles = b0 + lane < batch ? (cached(x, b0 + lane) + nodes + KT - 1) / KT : 0;
+    const int runs = (tiles + size - 1) / size;
+    int incl = runs;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int up = __shfl_up(incl, o);
+      if (lane >= o) incl += up;
+    }
+    const uint64_t hit = __ballot(base + incl > unit);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      r->b = b0 + at;
+      r->runs = __builtin_amdgcn_readlane(runs, at);
+      r->first = base + __builtin_amdgcn_readlane(incl, at) - r->runs;
+      const int t = __builtin_amdgcn_readlane(tiles, at), each = (t + r->runs - 1) / r->runs;
+      r->begin = min(t, (unit - r->first) * each);
+      r->end = min(t, r->begin + each);
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// Shared memory holds rows of DP elements in 16-byte chunks; chunk c of row r stands at
+// c ^ (a function of r), so that neither the 16 rows x 16 bytes that a matrix operand of keys
+// takes at once nor the 8 rows x 32 bytes of a transposing load meet in a bank.
+template <int DP>
+__device__ __forceinline__ int key_chunk(int r, int c) { return c ^ (DP == 64 ? (r >> 1) & 7 : r & 15); }
+template <int DP>
+__device__ __forceinline__ int value_chunk(int r, int c) { return c ^ (DP == 64 ? ((r >> 1) & 3) << 1 : (r & 7) << 1); }
+
+// Four neighbouring columns' worth of 16-bit infinities and NaN to zero; whether any was.
+template <int DT>
+__device__ __forceinline__ bool drop_nonfinite(u32x4& v) {
+  constexpr uint32_t top = DT == TF_DT_F16 ? 0x7C00u : 0x7F80u;
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t u = v[i];
+    if ((u & top) == top) u &= 0xFFFF0000u, any = true;
+    if ((u & top << 16) == top << 16) u &= 0xFFFFu, any = true;
+    v[i] = u;
+  }
+  return any;
+}
+
+// Bits 0 .. 3: whether a row of mask `seen` sees the positions that begin `node` behind the
+// cache's end (before it where negative), `left` before the run's.
+__device__ __forceinline__ uint32_t seen_of(uint64_t seen, int node, int left) {
+  const uint32_t tree = node >= 0 ? (uint32_t)(seen >> min(node, 63)) : ((uint32_t)seen << min(-node, 4)) | ((1u << min(-node, 4)) - 1);
+  return tree & (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1);
+}
+
+template <int DT, int DP, int RT, int RG, int KG, int KW>
+__global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) {
+  typedef uint16_t T;
+  constexpr int kThreads = RG * KG * 64, KT = KG * KW, NC = DP / 8, NK = KW / 16, NB = KW / 32, ND = DP / 16, NQ = DP / 32;
+  constexpr int kStep = kThreads / NC, kLoads = KT / kStep;  // rows between a thread's loads, and how many
+  static_assert(KT % kStep == 0 && KW % 32 == 0, "");
+  constexpr int kTile = KT * NC;
+  constexpr int kJoin = KG > 1 ? (KG - 1) * RG * ND * 64 : 0;  // other key groups' outputs, one row tile at a time
+  __shared__ u32x4 lds[2 * kTile > kJoin ? 2 * kTile : kJoin];
+  __shared__ float2 join_stat[KG > 1 ? (KG - 1) * RG * 64 : 1];
+  __shared__ int odd_values;
+
+  // Row tiles of one run go to one XCD (workgroups go round the eight of them), whose L2
+  // then serves the run's keys and values to all but the first.
+  ArgPtr x = arguments();
+  const int kv_heads = x->a.kv_heads, nodes = x->a.nodes;
+  const int k = blockIdx.x >> 3, up = copy(&x->p.by_row_tiles).div(k);
+  const int row_tile = k - up * x->p.row_tiles, uh = up * 8 + (blockIdx.x & 7);
+  const int unit = copy(&x->p.by_heads).div(uh), g = uh - unit * kv_heads;
+  if (unit >= x->p.units) return;
+  Run run;
+  if (!find_run<KT>(x, unit, &run)) return;
+  const int b = run.b, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int rg = wave % RG, kg = wave / RG, lg = lane >> 4;
+  if (x->p.target && unit == run.first && g == 0 && row_tile == 0 && tid == 0) x->p.seq[b] = make_int2(run.first, run.runs);
+  const int len = cached(x, b);
+  const int stop = min(run.end * KT, len + nodes);  // positions of the run: begin * KT .. stop - 1
+  if (tid == 0) odd_values = 0;
+
+  // The rows' queries and masks.
+  const int row0 = (row_tile * RG + rg) * 16 * RT;
+  const bool active = row0 < x->p.rows;
+  u32x4 q[RT][NQ];
+  uint64_t seen[RT];
+  {
+    const int rows = x->p.rows, group = x->p.group, dim = x->a.head_dim;
+    const FastDiv by_group = copy(&x->p.by_group);
+    const uint32_t flip = x->p.negate ? 0x80008000u : 0u;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = row0 + rt * 16 + (lane & 15), have = min(r, rows - 1);
+      const int node = by_group.div(have), head = g * group + have - node * group;
+      const T* row = static_cast<const T*>(x->a.q) + b * x->a.q_stride[0] + node * x->a.q_stride[1] + head * x->a.q_stride[2];
+      seen[rt] = r < rows ? (uint64_t)x->a.mask[(int64_t)b * nodes + node] : 0;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int d = i * 32 + lg * 8;
+        q[rt][i] = u32x4(0u);
+        if (r < rows && d < dim) q[rt][i] = *reinterpret_cast<const u32x4*>(row + d);
+        q[rt][i] ^= flip;
+      }
+    }
+  }
+
+  // The loader's part: chunk `chunk` of rows tid / NC, + kStep, ...
+  const int chunk = tid % NC, lrow = tid / NC;
+  x = arguments();
+  const float scale_c = x->p.c;
+  const bool have = chunk * 8 < x->a.head_dim;
+  const T* kc = static_cast<const T*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * 8;
+  const T* vc = static_cast<const T*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * 8;
+  const int64_t kc_page = x->a.k_cache_stride[0], kc_slot = x->a.k_cache_stride[1];
+  const int64_t vc_page = x->a.v_cache_stride[0], vc_slot = x->a.v_cache_stride[1];
+  const int32_t* table = x->a.table + b * x->a.table_stride;
+  const int pages = x->a.pages, page_size = x->a.page_size;
+  const FastDiv by_page = copy(&x->p.by_page);
+  u32x4 kr[kLoads], vr[kLoads];
+  int page[kLoads] = {};
+  // Columns of the table for the tile at `at`; the nodes' rows look the last one up.
+  auto look_up = [&](int at) {
+    if (len > 0) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) page[i] = table[by_page.div(min(at + lrow + i * kStep, len - 1))];
+    }
+  };
+  // A tile's rows; behind the run's end the last row again, which is not used.
+  auto load = [&](int at) {
+    const bool edge = at + KT > min(len, stop);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = edge ? min(at + lrow + i * kStep, stop - 1) : at + lrow + i * kStep;
+      const int64_t pg = (uint32_t)page[i] < (uint32_t)pages ? page[i] : 0;
+      const int64_t slot = j - by_page.div(j) * page_size;
+      const T* kp = kc + pg * kc_page + slot * kc_slot;
+      const T* vp = vc + pg * vc_page + slot * vc_slot;
+      if (edge) {
+        const ArgPtr y = arguments();
+        const T* kt = static_cast<const T*>(y->a.k) + b * y->a.k_stride[0] + g * y->a.k_stride[2] + (j - len) * y->a.k_stride[1] + chunk * 8;
+        const T* vt = static_cast<const T*>(y->a.v) + b * y->a.v_stride[0] + g * y->a.v_stride[2] + (j - len) * y->a.v_stride[1] + chunk * 8;
+        kp = j < len ? kp : kt;
+        vp = j < len ? vp : vt;
+      }
+      kr[i] = *reinterpret_cast<const u32x4*>(kp);
+      vr[i] = *reinterpret_cast<const u32x4*>(vp);
+    }
+  };
+
+  f32x4 o[ND][RT];
+  float m[RT], z[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY, z[rt] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) o[dt][rt] = f32x4(0.f);
+  }
+  const u32x4* key_row = lds + (kg * KW + (lane & 15)) * NC;
+  const int vrow = lg * 4 + ((lane & 15) >> 2);  // of the 32 positions of a step, and 16 behind
+  const u32x4* value_row = lds + kTile + (kg * KW + vrow) * NC;
+
+  int at = run.begin * KT;
+  if (have) {
+    look_up(at);
+    load(at);
+    look_up(at + KT);
+  } else {
+    // Columns behind the head's are zero throughout.
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = lrow + i * kStep;
+      lds[r * NC + key_chunk<DP>(r, chunk)] = u32x4(0u);
+      lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = u32x4(0u);
+    }
+  }
+  for (; at < stop; at += KT) {
+    const bool edge = at + KT > min(len, stop);
+    __syncthreads();  // the last tile has been used
+    if (have) {
+      if (edge) {
+        // A node's values that are no numbers would reach the rows that do not see it as 0 times
+        // them; they are put back below.
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int j = at + lrow + i * kStep;
+          if (j >= stop) vr[i] = u32x4(0u);
+          if (j >= len && drop_nonfinite<DT>(vr[i])) odd_values = 1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = lrow + i * kStep;
+        lds[r * NC + key_chunk<DP>(r, chunk)] = kr[i];
+        lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = vr[i];
+      }
+      if (at + KT < stop) {
+        load(at + KT);
+        look_up(at + 2 * KT);
+      }
+    }
+    __syncthreads();
+    if (!active) continue;
+
+    f32x4 s[NK][RT];
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s[t][rt] = f32x4(0.f);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int t = 0; t < NK; ++t) {
+        const u32x4 kf = key_row[t * 16 * NC + key_chunk<DP>(lane & 15, i * 4 + lg)];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[t][rt] = mfma<DT>(kf, q[rt][i], s[t][rt]);
+      }
+
+    if (edge) {
+#pragma unroll
+      for (int t = 0; t < NK; ++t) {
+        const int j = at + kg * KW + t * 16 + lg * 4;  // the first of the lane's four
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const uint32_t bits = seen_of(seen[rt], j - len, stop - j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[t][rt][i] = (bits >> i) & 1 ? s[t][rt][i] : -INFINITY;
+        }
+      }
+    }
+
+    float top[RT];
+    bool grow = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float v = s[0][rt][0];
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v = fmaxf(v, s[t][rt][i]);
+      top[rt] = fmaxf(m[rt], groups_max(v));
+      grow = grow || top[rt] > m[rt];
+    }
+    if (__ballot(grow)) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float keep = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - top[rt]) * scale_c);
+        m[rt] = top[rt];
+        z[rt] *= keep;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
+      }
+    }
+    u32x4 pf[NB][RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const float mc = m[rt] == -INFINITY ? 0.f : m[rt] * scale_c;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < NK; ++t) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], scale_c, -mc));
+          sum += e[i];
+        }
+        pf[t / 2][rt][(t & 1) * 2] = pack2<DT>(e[0], e[1]);
+        pf[t / 2][rt][(t & 1) * 2 + 1] = pack2<DT>(e[2], e[3]);
+      }
+      z[rt] += sum;
+    }
+#pragma unroll
+    for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) {
+        // chunks 2 dt and 2 dt + 1 of the row, 8 bytes a lane
+        const u32x4* row = value_row + kb * 32 * NC + value_chunk<DP>(vrow, dt * 2 + ((lane & 3) >> 1));
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row) + (lane & 1)));
+        const s16x4 hi =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row + 16 * NC) + (lane & 1)));
+        const u32x4 vf = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[dt][rt] = mfma<DT>(vf, pf[kb][rt], o[dt][rt]);
+      }
+  }
+
+  __syncthreads();
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) z[rt] = groups_sum(z[rt]);
+  if constexpr (KG > 1) {
+    // Key group 0 takes in the others' rows, in order.
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      __syncthreads();
+      if (kg > 0) {
+        const int w = (kg - 1) * RG + rg;
+        join_stat[w * 64 + lane] = make_float2(m[rt], z[rt]);
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) lds[(w * ND + dt) * 64 + lane] = __builtin_bit_cast(u32x4, o[dt][rt]);
+      }
+      __syncthreads();
+      if (kg == 0) {
+#pragma unroll
+        for (int other = 0; other < KG - 1; ++other) {
+          const int w = other * RG + rg;
+          const float2 st = join_stat[w * 64 + lane];
+          const float top = fmaxf(m[rt], st.x);
+          const float mine = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - top) * scale_c);
+          const float its = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.x - top) * scale_c);
+          m[rt] = top;
+          z[rt] = z[rt] * mine + st.y * its;
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt)
+            o[dt][rt] = o[dt][rt] * mine + __builtin_bit_cast(f32x4, lds[(w * ND + dt) * 64 + lane]) * its;
+        }
+      }
+    }
+    if (kg > 0) return;
+  }
+  if (!active) return;
+
+  x = arguments();
+  const int dim = x->a.head_dim;
+  if (odd_values) {
+    for (int j = max(len, run.begin * KT); j < stop; ++j) {
+      const T* row = static_cast<const T*>(x->a.v) + b * x->a.v_stride[0] + g * x->a.v_stride[2] + (j - len) * x->a.v_stride[1];
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) {
+        if (dt * 16 >= dim) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = Elem<DT>::load(row[dt * 16 + lg * 4 + i]), odd = fabsf(v) < INFINITY ? 0.f : v;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) o[dt][rt][i] += (seen[rt] >> (j - len)) & 1 ? odd : 0.f;
+        }
+      }
+    }
+  }
+
+  const int rows = x->p.rows, group = x->p.group;
+  const FastDiv by_group = copy(&x->p.by_group);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = row0 + rt * 16 + (lane & 15);
+    if (r >= rows) continue;
+    if (run.runs == 1) {
+      const int node = by_group.div(r), head = g * group + r - node * group;
+      T* out = static_cast<T*>(x->a.out) + b * x->a.out_stride[0] + node * x->a.out_stride[1] + head * x->a.out_stride[2] + lg * 4;
+      const float inv = z[rt] == 0.f ? 0.f : 1.f / z[rt];
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt)
+        if (dt * 16 < dim) {
+          const f32x4 v = z[rt] == 0.f ? f32x4(0.f) : o[dt][rt] * inv;
+          *reinterpret_cast<u32x2*>(out + dt * 16) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+        }
+    } else {
+      const int64_t row = ((int64_t)unit * kv_heads + g) * rows + r;
+      if (lg == 0) x->p.stat[row] = make_float2(m[rt] == -INFINITY ? -INFINITY : m[rt] * scale_c, z[rt]);
+      float* part = x->p.part + row * dim + lg * 4;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt)
+        if (dt * 16 < dim) *reinterpret_cast<f32x4*>(part + dt * 16) = o[dt][rt];
+    }
+  }
+}
+
+// Four columns of one row a thread: its runs, joined in order.
+template <int DT>
+__global__ __launch_bounds__(256) void tree_attention_join_kernel(tf_exl3_tree_attention_args a, AttnPlan p) {
+  const int b = blockIdx.y, f = blockIdx.x * 256 + threadIdx.x;
+  const int row = p.by_quads.div(f), d = (f - row * (a.head_dim / 4)) * 4;  // row: (head, row of the head)
+  if (row >= a.kv_heads * p.rows) return;
+  const int2 seq = p.seq[b];
+  if (seq.y == 1) return;
+  const int64_t first = (int64_t)seq.x * a.kv_heads * p.rows + row, step = (int64_t)a.kv_heads * p.rows;
+  float top = -INFINITY;
+  for (int i = 0; i < seq.y; ++i) top = fmaxf(top, p.stat[first + i * step].x);
+  float z = 0.f;
+  f32x4 o = f32x4(0.f);
+  for (int i = 0; i < seq.y; ++i) {
+    const float2 st = p.stat[first + i * step];
+    const float w = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.x - top);
+    z = __builtin_fmaf(st.y, w, z);
+    o += *reinterpret_cast<const f32x4*>(p.part + (first + i * step) * a.head_dim + d) * w;
+  }
+  const int g = row / p.rows, r = row - g * p.rows, node = p.by_group.div(r), head = g * p.group + r - node * p.group;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + node * a.out_stride[1] + head * a.out_stride[2] + d;
+  if (z == 0.f)
+    o = f32x4(0.f);
+  else
+    o *= 1.f / z;
+  *reinterpret_cast<u32x2*>(out) = u32x2{pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3])};
+}
+
+namespace {
+
+// How a call's rows and positions are spread; by the sizes alone.
+struct Shape {
+  int dp, rt, rg, kg, kw;
+  int tile() const { return kg * kw; }
+  int rows() const { return 16 * rt * rg; }
+};
+
+Shape shape_of(int dim, int rows) {
+  const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+  // (A wave of one row group holds 32 positions at 256 columns in half its registers.)
+  if (rows <= 16 && dp < 256) return {dp, 1, 1, 2, 32};
+  if (rows <= 32) return {dp, 1, 2, 2, 32};
+  if (rows <= 64 || dp == 256) return {dp, 1, 4, 1, 64};
+  const int two = (rows + 127) / 128 * 2, three = (rows + 191) / 192 * 3;  // row tiles of 64 that are computed
+  return {dp, two < three ? 2 : 3, 4, 2, 32};
+}
+
+constexpr int kCUs = 256;
+
+struct Layout {
+  Shape s;
+  AttnPlan p;
+  size_t seq_bytes, stat_bytes, part_bytes;
+};
+
+Layout layout_of(const tf_exl3_tree_attention_args& a) {
+  Layout l;
+  const int group = a.q_heads / a.kv_heads, rows = a.nodes * group;
+  l.s = shape_of(a.head_dim, rows);
+  AttnPlan& p = l.p;
+  p.rows = rows, p.group = group;
+  p.row_tiles = (rows + l.s.rows() - 1) / l.s.rows();
+  const int64_t room = (int64_t)a.table_pages * a.page_size + a.nodes;
+  const int64_t groups = (int64_t)a.kv_heads * p.row_tiles;  // workgroups of a run
+  // Runs enough for every CU to have as many workgroups as fit it, but none so short that
+  // writing and joining its rows would cost as much as reading its positions.
+  const int64_t slots = kCUs * (l.s.rt > 1 ? 1 : 4);
+  p.min_tiles = l.s.rt > 1 ? 8 : 1;
+  const int64_t run = (int64_t)p.min_tiles * l.s.tile(), most = a.batch * ((room + run - 1) / run);
+  const int64_t target = (slots + groups - 1) / groups;
+  p.target = (int)(target < most ? target : most);
+  if (a.batch > 1024 || p.target <= a.batch / 4 || room <= run) p.target = 0;
+  p.units = a.batch + p.target;
+  const size_t n = p.target ? (size_t)p.units * a.kv_heads * rows : 0;
+  l.seq_bytes = ((size_t)a.batch * sizeof(int2) + 15) / 16 * 16;
+  l.stat_bytes = (n * sizeof(float2) + 15) / 16 * 16;
+  l.part_bytes = n * a.head_dim * sizeof(float);
+  return l;
+}
+
+template <int DT, int DP, int RT, int RG, int KG, int KW>
+void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t stream) {
+  const int64_t runs = ((int64_t)p.units * a.kv_heads + 7) / 8 * 8;
+  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW>), dim3((unsigned)(runs * p.row_tiles)), dim3(RG * KG * 64), 0,
+                     stream, AttnArgs{a, p});
+}
+
+template <int DT, int DP>
+void launch_dim(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream_t stream) {
+  const Shape& s = l.s;
+  if constexpr (DP < 256) {
+    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32>(a, l.p, stream);
+  }
+  if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32>(a, l.p, stream);
+  if (s.rt == 1) return launch<DT, DP, 1, 4, 1, 64>(a, l.p, stream);
+  if constexpr (DP < 256) {
+    if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32>(a, l.p, stream);
+    return launch<DT, DP, 3, 4, 2, 32>(a, l.p, stream);
+  }
+}
+
+template <int DT>
+void launch_type(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream_t stream) {
+  if (l.s.dp == 64)
+    launch_dim<DT, 64>(a, l, stream);
+  else if (l.s.dp == 128)
+    launch_dim<DT, 128>(a, l, stream);
+  else
+    launch_dim<DT, 256>(a, l, stream);
+  if (l.p.target == 0) return;
+  const int64_t quads = (int64_t)a.kv_heads * l.p.rows * (a.head_dim / 4);
+  hipLaunchKernelGGL(tree_attention_join_kernel<DT>, dim3((unsigned)((quads + 255) / 256), a.batch), dim3(256), 0, stream, a, l.p);
+}
+
+}  // namespace
+
+size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a) {
+  const Layout l = layout_of(a);
+  return l.seq_bytes + l.stat_bytes + l.part_bytes + 16;
+}
 
 hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream) {
-  const dim3 grid(a.q_heads, a.nodes, a.batch), block(64);
+  Layout l = layout_of(a);
+  const int64_t runs = ((int64_t)l.p.units * a.kv_heads + 7) / 8 * 8;
+  if (runs * l.p.row_tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  char* ws = static_cast<char*>(a.workspace);
+  l.p.seq = reinterpret_cast<int2*>(ws);
+  l.p.stat = reinterpret_cast<float2*>(ws + l.seq_bytes);
+  l.p.part = reinterpret_cast<float*>(ws + l.seq_bytes + l.stat_bytes);
+  // A scale of 0 keeps masked scores apart from others: the smallest factor does the same to sums.
+  const float c = fabsf(a.scale) * 1.4426950408889634f;
+  l.p.c = c > 1.2e-38f ? c : 1.2e-38f;
+  l.p.negate = a.scale < 0.f;
+  l.p.by_group = fast_div(l.p.group), l.p.by_page = fast_div(a.page_size);
+  l.p.by_row_tiles = fast_div(l.p.row_tiles), l.p.by_heads = fast_div(a.kv_heads);
+  l.p.by_quads = fast_div(a.head_dim / 4);
   if (a.dtype == TF_DT_F16)
-    hipLaunchKernelGGL(tree_attention_kernel<TF_DT_F16>, grid, block, 0, stream, a);
+    launch_type<TF_DT_F16>(a, l, stream);
   else
-    hipLaunchKernelGGL(tree_attention_kernel<TF_DT_BF16>, grid, block, 0, stream, a);
+    launch_type<TF_DT_BF16>(a, l, stream);
   return hipGetLastError();
 }
 
