@@ -3,6 +3,7 @@
 // With d = x - max x, the student's p[i] = 2^(d c) / z, c = log2(e) / T, z their sum; a
 // row's loss and gradient need z and the maximum before anything can be written, so a
 // row is read, held on chip where it fits, and the gradient written from what is held.
+// Bound by the logits' bytes, read once and, with the gradient, written once.
 #include <math.h>
 
 #include "ops_device.hpp"
@@ -11,24 +12,16 @@
 namespace tf_exl3 {
 
 constexpr int kMaxTop = 1024;
+constexpr int kGroupElems = 16;  // held elements that are summed by one maximum
 
 // 2^(d c) with c in two parts: the product's error is then one rounding of the
 // exponent and not the rounding of c times |d|, which all elements would share.
 struct Scale {
   float inv, c, c_low;
-  __device__ float exp(float d) const {
-    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, c, d * c_low));
-  }
+  __device__ float exp(float d) const { return __builtin_amdgcn_exp2f(__builtin_fmaf(d, c, d * c_low)); }
 };
 
-__device__ __forceinline__ Scale scale_of(float temperature) {
-  Scale s;
-  const double c = 1.4426950408889634 / (double)temperature;
-  s.inv = 1.f / temperature;
-  s.c = (float)c;
-  s.c_low = (float)(c - (double)s.c);
-  return s;
-}
+__device__ __forceinline__ Scale scale_of(const DistillArgs& a) { return {a.inv, a.c, a.c_low}; }
 
 template <int N>
 __device__ __forceinline__ float max_of(const float (&x)[N], float m) {
@@ -47,79 +40,166 @@ __device__ __forceinline__ float sum_of(float (&s)[N]) {
   return s[0];
 }
 
+// A running maximum m and sums s of 2^((x - m) c), taken on by M pieces.
+template <int DT, int M>
+__device__ __forceinline__ void take(const u32x4* v, const Scale& sc, float& m, float (&s)[Elem<DT>::kPiece]) {
+  constexpr int P = Elem<DT>::kPiece;
+  float e[M][P], top = m;
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    Elem<DT>::unpack(v[i], e[i]);
+    top = max_of(e[i], top);
+  }
+  const float base = top == -INFINITY ? 0.f : top, keep = sc.exp(m - base);
+#pragma unroll
+  for (int c = 0; c < P; ++c) s[c] *= keep;
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+#pragma unroll
+    for (int c = 0; c < P; ++c) s[c] += sc.exp(e[i][c] - base);
+  m = top;
+}
+
+// The teacher's entries of a row. Its probabilities do not depend on the student: the first
+// wave works them out while the row is on its way. In the gradient an entry is met again by
+// the thread that writes the piece with its place, so each thread has a list of its entries.
+template <int THREADS>
 struct Teacher {
-  float t[kMaxTop];  // logit, then probability
-  int at[kMaxTop];   // place, -1 for an entry that is left out
+  float t[kMaxTop + 8];  // probability; eight left out entries stand behind the last
+  int at[kMaxTop + 8];   // place, -1 for an entry that is left out
+  float all[kMaxTop];    // sum of the probabilities at its place
+  int next[kMaxTop], head[THREADS];
+  int none;  // no entry at all
 };
 
-// The teacher's entries into shared memory.
-template <int THREADS>
-__device__ __forceinline__ void load_teacher(const DistillArgs& a, int64_t r, Teacher& s) {
-  for (int j = threadIdx.x; j < a.top_k; j += THREADS) {
+// The first wave's part. A lane's first entry is loaded ahead, into registers.
+template <int DT>
+struct Entries {
+  typedef typename Elem<DT>::type T;
+  int at0;
+  float y0, x0;
+  float ymax, ysum;
+
+  __device__ __forceinline__ int place(const DistillArgs& a, int64_t r, int j) const {
     const int i = a.index[r * a.top_k + j];
-    const bool there = i >= 0 && i < a.vocab;
-    s.at[j] = there ? i : -1;
-    s.t[j] = there ? load_elem(a.top, a.top_dtype, r * a.top_k + j) : -INFINITY;
+    return i >= 0 && i < a.vocab ? i : -1;
   }
-}
-
-// Its probabilities and the row's loss, given the student's maximum and sum. Each thread
-// meets only entries of its own until the barrier inside the last sum.
-template <int THREADS, int DT>
-__device__ __forceinline__ float teacher_loss(const DistillArgs& a, const Scale& sc, const typename Elem<DT>::type* x,
-                                              float top, float z, Teacher& s, float* red, bool* none) {
-  constexpr int kWaves = THREADS / 64;
-  float ymax = -INFINITY;
-  for (int j = threadIdx.x; j < a.top_k; j += THREADS) ymax = fmaxf(ymax, s.t[j]);
-  ymax = block_max<kWaves>(ymax, red);
-  float ysum = 0.f;
-  for (int j = threadIdx.x; j < a.top_k; j += THREADS) ysum += s.at[j] >= 0 ? sc.exp(s.t[j] - ymax) : 0.f;
-  ysum = block_sum<kWaves>(ysum, red);
-  *none = ysum == 0.f;
-  const float lz = logf(z), lys = logf(ysum);
-  float loss = 0.f;
-  for (int j = threadIdx.x; j < a.top_k; j += THREADS) {
-    float t = 0.f;
-    if (s.at[j] >= 0) {
-      const float ly = (s.t[j] - ymax) * sc.inv - lys;
-      t = sc.exp(s.t[j] - ymax) / ysum;
-      if (t > 0.f) loss += t * (ly - ((Elem<DT>::load(x[s.at[j]]) - top) * sc.inv - lz));
+  __device__ __forceinline__ float logit(const DistillArgs& a, int64_t r, int j) const {
+    return load_elem(a.top, a.top_dtype, r * a.top_k + j);
+  }
+  __device__ __forceinline__ void begin(const DistillArgs& a, int64_t r) {
+    at0 = -1, y0 = x0 = 0.f;
+    if ((int)threadIdx.x < a.top_k && threadIdx.x < 64) at0 = a.index[r * a.top_k + threadIdx.x], y0 = logit(a, r, threadIdx.x);
+  }
+  // Probabilities into shared memory; the student's logit at the first entry on its way.
+  template <int THREADS>
+  __device__ __forceinline__ void softmax(const DistillArgs& a, const Scale& sc, int64_t r, const T* x, Teacher<THREADS>& s) {
+    const int lane = threadIdx.x;
+    if (at0 >= a.vocab || at0 < 0) at0 = -1, y0 = -INFINITY;
+    if (at0 >= 0) x0 = Elem<DT>::load(x[at0]);
+    bool any = at0 >= 0;
+    ymax = y0;
+    if (lane < a.top_k) s.at[lane] = at0;
+    for (int j = lane + 64; j < a.top_k; j += 64) {
+      const int at = place(a, r, j);
+      s.at[j] = at;
+      s.t[j] = at >= 0 ? logit(a, r, j) : -INFINITY;
+      any = any || at >= 0;
+      ymax = fmaxf(ymax, s.t[j]);
     }
-    s.t[j] = t;
+    if (lane < 8) s.at[a.top_k + lane] = -1, s.t[a.top_k + lane] = 0.f;
+    ymax = wave_max(lane < a.top_k ? ymax : -INFINITY);
+    const uint64_t some = __ballot(any);
+    if (lane == 0) s.none = some == 0;
+    ysum = at0 >= 0 ? sc.exp(y0 - ymax) : 0.f;
+    for (int j = lane + 64; j < a.top_k; j += 64) ysum += s.at[j] >= 0 ? sc.exp(s.t[j] - ymax) : 0.f;
+    ysum = wave_sum(ysum);
+    if (lane < a.top_k) s.t[lane] = at0 >= 0 ? sc.exp(y0 - ymax) / ysum : 0.f;
+    for (int j = lane + 64; j < a.top_k; j += 64) s.t[j] = s.at[j] >= 0 ? sc.exp(s.t[j] - ymax) / ysum : 0.f;
   }
-  return block_sum<kWaves>(loss, red);
-}
+  // The row's loss, in lane 63, given the student's maximum and sum.
+  template <int THREADS>
+  __device__ __forceinline__ float loss(const DistillArgs& a, const Scale& sc, int64_t r, const T* x, float top, float z,
+                                        const Teacher<THREADS>& s) const {
+    const int lane = threadIdx.x;
+    const float lz = logf(z), lys = logf(ysum);
+    auto term = [&](int j, float y, float xj) {
+      const float t = s.t[j];
+      return t > 0.f ? t * ((y - ymax) * sc.inv - lys - ((xj - top) * sc.inv - lz)) : t;  // a NaN stays one
+    };
+    float sum = at0 >= 0 ? term(lane, y0, x0) : 0.f;
+    for (int j = lane + 64; j < a.top_k; j += 64)
+      if (s.at[j] >= 0) sum += term(j, logit(a, r, j), Elem<DT>::load(x[s.at[j]]));
+    return wave_scan(sum);
+  }
+};
 
-// The gradient at the teacher's places within [lo, hi), over what the row's pieces left
-// there. The first of equal places holds the sum of them all, in order.
-template <int THREADS, int DT>
-__device__ __forceinline__ void teacher_grad(const DistillArgs& a, const Scale& sc, const typename Elem<DT>::type* x,
-                                             typename Elem<DT>::type* grad, float top, float z, float w, const Teacher& s,
-                                             int lo, int hi) {
+// Entries with places in the pieces [lo, hi), each place once, into the lists of the threads
+// that write them: the piece's number modulo THREADS, or a row's last elements in order.
+template <int P, int THREADS>
+__device__ __forceinline__ void link(const DistillArgs& a, Teacher<THREADS>& s, int pieces, int64_t lo, int64_t hi) {
   for (int j = threadIdx.x; j < a.top_k; j += THREADS) {
-    const int at = s.at[j];
-    if (at < lo || at >= hi) continue;
+    const int at = s.at[j], piece = at / P;
+    if (at < 0 || piece < lo || piece >= hi) continue;
     float t = 0.f;
     bool first = true;
-    for (int i = 0; i < a.top_k; ++i)
-      if (s.at[i] == at) {
-        first = first && i >= j;
-        t += s.t[i];
+    for (int i0 = 0; i0 < a.top_k; i0 += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool same = s.at[i0 + i] == at;
+        first = first && !(same && i0 + i < j);
+        t += same ? s.t[i0 + i] : 0.f;
       }
-    if (first) grad[at] = Elem<DT>::store((sc.exp(Elem<DT>::load(x[at]) - top) / z - t) * w);
+    }
+    if (!first) continue;
+    s.all[j] = t;
+    s.next[j] = atomicExch(&s.head[piece < pieces ? piece % THREADS : at - pieces * P], j);
   }
 }
 
-template <int DT>
-__device__ __forceinline__ u32x4 grad_piece(u32x4 v, const Scale& sc, float top, float w_z, bool zero) {
-  constexpr int P = Elem<DT>::kPiece;
-  if (zero) return u32x4(0u);  // whatever the row holds
-  float e[P];
-  Elem<DT>::unpack(v, e);
+// What a thread writes of a row's gradient.
+template <int DT, int THREADS>
+struct Writer {
+  static constexpr int P = Elem<DT>::kPiece;
+  const Scale sc;
+  const Teacher<THREADS>& s;
+  float top, z, w, w_z;
+  bool zero;
+  int piece, at, next;  // of the list's first entry
+  float t;
+
+  __device__ __forceinline__ Writer(const Scale& scale, const Teacher<THREADS>& teach, float top_, float z_, float weight)
+      : sc(scale), s(teach), top(top_), z(z_), w(teach.none ? 0.f : weight * scale.inv), w_z(w / z_), zero(w == 0.f) {
+    const int j = s.head[threadIdx.x];
+    piece = at = next = -1, t = 0.f;
+    if (j >= 0) at = s.at[j], piece = at / P, t = s.all[j], next = s.next[j];
+  }
+  __device__ __forceinline__ void fix(const float (&x)[P], float (&g)[P], int at, float t) const {
 #pragma unroll
-  for (int i = 0; i < P; ++i) e[i] = sc.exp(e[i] - top) * w_z;
-  return Elem<DT>::pack(e);
-}
+    for (int c = 0; c < P; ++c)
+      if (at % P == c) g[c] = (sc.exp(x[c] - top) / z - t) * w;
+  }
+  __device__ __forceinline__ u32x4 operator()(u32x4 v, int64_t p) const {
+    if (zero) return u32x4(0u);  // whatever the row holds
+    float x[P], g[P];
+    Elem<DT>::unpack(v, x);
+#pragma unroll
+    for (int c = 0; c < P; ++c) g[c] = sc.exp(x[c] - top) * w_z;
+    if (p == piece) fix(x, g, at, t);
+    if (next >= 0) {  // seldom
+      for (int j = next; j >= 0; j = s.next[j])
+        if (p == s.at[j] / P) fix(x, g, s.at[j], s.all[j]);
+    }
+    return Elem<DT>::pack(g);
+  }
+  __device__ __forceinline__ typename Elem<DT>::type last(float x, int pieces) const {
+    if (zero) return Elem<DT>::store(0.f);
+    float total = piece == pieces ? t : 0.f;
+    for (int j = next; j >= 0; j = s.next[j])
+      if (s.at[j] / P == pieces) total = s.all[j];
+    return Elem<DT>::store((sc.exp(x - top) / z - total) * w);
+  }
+};
 
 // One workgroup per row, N pieces of 16 bytes held by each thread; what a longer row has
 // beyond them is read first, with a running maximum, and once more for the gradient
@@ -127,31 +207,26 @@ __device__ __forceinline__ u32x4 grad_piece(u32x4 v, const Scale& sc, float top,
 // sums' order depends on the row's length alone, so the loss has the same bits with and
 // without the gradient.
 template <int DT, int THREADS, int N>
-__global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs a) {
+__global__ __launch_bounds__(THREADS, 4) void distill_row_kernel(DistillArgs a) {
   typedef typename Elem<DT>::type T;
   constexpr int P = Elem<DT>::kPiece, kWaves = THREADS / 64;
   __shared__ float red[kWaves];
-  __shared__ Teacher teach;
+  __shared__ Teacher<THREADS> teach;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x;
   const T* x = static_cast<const T*>(a.logits) + r * a.logits_stride;
-  const Scale sc = scale_of(a.temperature);
+  const Scale sc = scale_of(a);
   const int pieces = a.vocab / P, rest = a.vocab - pieces * P;
-  load_teacher<THREADS>(a, r, teach);
+  Entries<DT> entries;
+  entries.begin(a, r);
+  teach.head[tid] = -1;
 
   float m = -INFINITY, s[P] = {};
   for (int i = N * THREADS + tid; i < pieces; i += 2 * THREADS) {
-    const bool two = i + THREADS < pieces;
-    const u32x4 v0 = load_piece(x + (int64_t)i * P);
-    const u32x4 v1 = two ? load_piece(x + (int64_t)(i + THREADS) * P) : u32x4(Elem<DT>::kMinusInf);
-    float e0[P], e1[P];
-    Elem<DT>::unpack(v0, e0);
-    Elem<DT>::unpack(v1, e1);
-    const float top = max_of(e1, max_of(e0, m)), base = top == -INFINITY ? 0.f : top;
-    const float keep = sc.exp(m - base);
-#pragma unroll
-    for (int c = 0; c < P; ++c) s[c] = __builtin_fmaf(s[c], keep, sc.exp(e0[c] - base) + sc.exp(e1[c] - base));
-    m = top;
+    u32x4 v[2];
+    v[0] = load_piece(x + (int64_t)i * P);
+    v[1] = i + THREADS < pieces ? load_piece(x + (int64_t)(i + THREADS) * P) : u32x4(Elem<DT>::kMinusInf);
+    take<DT, 2>(v, sc, m, s);
   }
   u32x4 v[N];
 #pragma unroll
@@ -160,44 +235,36 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(DistillArgs a) {
     if (i * THREADS + tid < pieces) v[i] = load_piece(x + (int64_t)(i * THREADS + tid) * P);
   }
   const float last = tid < rest ? Elem<DT>::load(x[(int64_t)pieces * P + tid]) : -INFINITY;
-  float top = fmaxf(m, last);
+  if (tid < 64) entries.softmax(a, sc, r, x, teach);
+  // Pieces are summed as they come, by the thread's own maximum so far, so that this is
+  // done while the later ones are on their way.
+  constexpr int kGroup = kGroupElems / P;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i * THREADS < pieces) {
-      float e[P];
-      Elem<DT>::unpack(v[i], e);
-      top = max_of(e, top);
-    }
-  top = block_max<kWaves>(top, red);
+  for (int g = 0; g < N; g += kGroup)
+    if (g * THREADS < pieces) take<DT, kGroup>(v + g, sc, m, s);
+  const float top = block_max<kWaves>(fmaxf(m, last), red);
+  if (a.grad) link<P, THREADS>(a, teach, pieces, 0, (int64_t)pieces + 1);
   const float keep = m == -INFINITY ? 0.f : sc.exp(m - top);
 #pragma unroll
   for (int c = 0; c < P; ++c) s[c] *= keep;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i * THREADS < pieces) {
-      float e[P];
-      Elem<DT>::unpack(v[i], e);
-#pragma unroll
-      for (int c = 0; c < P; ++c) s[c] += sc.exp(e[c] - top);
-    }
   const float z = block_sum<kWaves>(sum_of(s) + sc.exp(last - top), red);
 
-  bool none;
-  const float loss = teacher_loss<THREADS, DT>(a, sc, x, top, z, teach, red, &none);
-  if (a.loss && tid == 0) a.loss[r] = loss;
+  if (tid < 64 && a.loss) {
+    const float loss = entries.loss(a, sc, r, x, top, z, teach);
+    if (tid == 63) a.loss[r] = loss;
+  }
   if (!a.grad) return;
 
   T* grad = static_cast<T*>(a.grad) + r * a.grad_stride;
-  const float w = none ? 0.f : a.weight[r] * sc.inv, w_z = w / z;
-  const bool zero = w == 0.f;
+  const Writer<DT, THREADS> out(sc, teach, top, z, a.weight[r]);
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i * THREADS + tid < pieces) store_piece(grad + (int64_t)(i * THREADS + tid) * P, grad_piece<DT>(v[i], sc, top, w_z, zero));
-  if (tid < rest) grad[(int64_t)pieces * P + tid] = Elem<DT>::store(zero ? 0.f : sc.exp(last - top) * w_z);
+  for (int i = 0; i < N; ++i) {
+    const int p = i * THREADS + tid;
+    if (p < pieces) store_piece(grad + (int64_t)p * P, out(v[i], p));
+  }
+  if (tid < rest) grad[(int64_t)pieces * P + tid] = out.last(last, pieces);
   for (int i = N * THREADS + tid; i < pieces; i += THREADS)
-    store_piece(grad + (int64_t)i * P, grad_piece<DT>(load_piece(x + (int64_t)i * P), sc, top, w_z, zero));
-  __syncthreads();
-  if (!zero) teacher_grad<THREADS, DT>(a, sc, x, grad, top, z, w, teach, 0, a.vocab);
+    store_piece(grad + (int64_t)i * P, out(load_piece(x + (int64_t)i * P), i));
 }
 
 // Few rows: each is cut into parts of kPart pieces, one workgroup each. The first launch
@@ -233,24 +300,16 @@ __global__ __launch_bounds__(kPartThreads) void distill_part_kernel(DistillArgs 
   __shared__ float red[kWaves];
   const int part = blockIdx.x;
   const int64_t r = blockIdx.y;
-  const Scale sc = scale_of(a.temperature);
+  const Scale sc = scale_of(a);
   u32x4 v[kPartPieces];
   float last;
   load_part<DT>(a, static_cast<const typename Elem<DT>::type*>(a.logits) + r * a.logits_stride, part, v, &last);
-  float e[kPartPieces][P], top = last;
-#pragma unroll
-  for (int i = 0; i < kPartPieces; ++i) {
-    Elem<DT>::unpack(v[i], e[i]);
-    top = max_of(e[i], top);
-  }
-  top = block_max<kWaves>(top, red);
+  float m = -INFINITY, s[P] = {};
+  take<DT, kPartPieces>(v, sc, m, s);
+  const float top = block_max<kWaves>(fmaxf(m, last), red);
   const float base = top == -INFINITY ? 0.f : top;  // a part without weight adds nothing
-  float s[P] = {};
-#pragma unroll
-  for (int i = 0; i < kPartPieces; ++i)
-#pragma unroll
-    for (int c = 0; c < P; ++c) s[c] += sc.exp(e[i][c] - base);
-  const float z = block_sum<kWaves>(sum_of(s) + sc.exp(last - base), red);
+  const float keep = m == -INFINITY ? 0.f : sc.exp(m - base);
+  const float z = block_sum<kWaves>(sum_of(s) * keep + sc.exp(last - base), red);
   if (threadIdx.x == 0) static_cast<PartStat*>(a.workspace)[r * gridDim.x + part] = {top, z};
 }
 
@@ -259,43 +318,48 @@ __global__ __launch_bounds__(kPartThreads) void distill_join_kernel(DistillArgs 
   typedef typename Elem<DT>::type T;
   constexpr int P = Elem<DT>::kPiece, kWaves = kPartThreads / 64;
   __shared__ float red[kWaves];
-  __shared__ Teacher teach;
+  __shared__ Teacher<kPartThreads> teach;
   const int part = blockIdx.x, tid = threadIdx.x;
   const int64_t r = blockIdx.y;
   const T* x = static_cast<const T*>(a.logits) + r * a.logits_stride;
-  const Scale sc = scale_of(a.temperature);
-  u32x4 v[kPartPieces];
-  float last;
-  if (a.grad) load_part<DT>(a, x, part, v, &last);
-  load_teacher<kPartThreads>(a, r, teach);
+  const Scale sc = scale_of(a);
+  const int pieces = a.vocab / P;
+  Entries<DT> entries;
+  entries.begin(a, r);
+  teach.head[tid] = -1;
   const PartStat* stat = static_cast<const PartStat*>(a.workspace) + r * parts;
-  float top = -INFINITY;
-  for (int i = tid; i < parts; i += kPartThreads) top = fmaxf(top, stat[i].top);
+  PartStat mine = {-INFINITY, 0.f};
+  if (tid < parts) mine = stat[tid];
+  u32x4 v[kPartPieces];
+  float last = -INFINITY;
+  if (a.grad) load_part<DT>(a, x, part, v, &last);
+  if (tid < 64) entries.softmax(a, sc, r, x, teach);
+  float top = mine.top;
+  for (int i = tid + kPartThreads; i < parts; i += kPartThreads) top = fmaxf(top, stat[i].top);
   top = block_max<kWaves>(top, red);
-  float z = 0.f;
-  for (int i = tid; i < parts; i += kPartThreads) z += stat[i].sum * sc.exp(stat[i].top - top);
+  const int64_t lo = (int64_t)part * kPart, hi = lo + kPart < pieces ? lo + kPart : pieces;
+  if (a.grad) {
+    link<P, kPartThreads>(a, teach, pieces, lo, hi);
+    if (part == 0) link<P, kPartThreads>(a, teach, pieces, pieces, (int64_t)pieces + 1);
+  }
+  float z = tid < parts ? mine.sum * sc.exp(mine.top - top) : 0.f;
+  for (int i = tid + kPartThreads; i < parts; i += kPartThreads) z += stat[i].sum * sc.exp(stat[i].top - top);
   z = block_sum<kWaves>(z, red);
-  bool none;
-  const float loss = teacher_loss<kPartThreads, DT>(a, sc, x, top, z, teach, red, &none);
-  if (a.loss && tid == 0 && part == 0) a.loss[r] = loss;
+  if (tid < 64 && part == 0 && a.loss) {
+    const float loss = entries.loss(a, sc, r, x, top, z, teach);
+    if (tid == 63) a.loss[r] = loss;
+  }
   if (!a.grad) return;
 
   T* grad = static_cast<T*>(a.grad) + r * a.grad_stride;
-  const float w = none ? 0.f : a.weight[r] * sc.inv, w_z = w / z;
-  const bool zero = w == 0.f;
-  const int pieces = a.vocab / P;
+  const Writer<DT, kPartThreads> out(sc, teach, top, z, a.weight[r]);
 #pragma unroll
   for (int i = 0; i < kPartPieces; ++i) {
-    const int64_t p = (int64_t)part * kPart + i * kPartThreads + tid;
-    if (p < pieces) store_piece(grad + p * P, grad_piece<DT>(v[i], sc, top, w_z, zero));
+    const int64_t p = lo + i * kPartThreads + tid;
+    if (p < pieces) store_piece(grad + p * P, out(v[i], p));
   }
   const int64_t at = (int64_t)pieces * P + tid;
-  if (part == 0 && at < a.vocab) grad[at] = Elem<DT>::store(zero ? 0.f : sc.exp(last - top) * w_z);
-  __syncthreads();
-  if (zero) return;
-  const int64_t lo = (int64_t)part * kPart * P, hi = lo + (int64_t)kPart * P;
-  teacher_grad<kPartThreads, DT>(a, sc, x, grad, top, z, w, teach, (int)lo, (int)(hi < pieces * (int64_t)P ? hi : pieces * (int64_t)P));
-  if (part == 0) teacher_grad<kPartThreads, DT>(a, sc, x, grad, top, z, w, teach, pieces * P, a.vocab);
+  if (part == 0 && at < a.vocab) grad[at] = out.last(last, pieces);
 }
 
 static int parts_of(int dtype, int vocab) {
@@ -305,10 +369,7 @@ static int parts_of(int dtype, int vocab) {
 
 // Rows that one workgroup each leave too few workgroups for the chip are cut.
 constexpr int kFewRows = 128;
-constexpr int kMaxParts = 65535;
-static bool cut(int dtype, int rows, int vocab) {
-  return rows <= kFewRows && parts_of(dtype, vocab) > 2 && parts_of(dtype, vocab) <= kMaxParts;
-}
+static bool cut(int dtype, int rows, int vocab) { return rows <= kFewRows && parts_of(dtype, vocab) > 2; }
 
 template <int DT>
 static void launch(const DistillArgs& a, hipStream_t stream) {
@@ -332,7 +393,10 @@ size_t distill_workspace(int dtype, int rows, int vocab, int) {
   return cut(dtype, rows, vocab) ? ((size_t)rows * parts_of(dtype, vocab) * sizeof(PartStat) + 15) / 16 * 16 : 16;
 }
 
-hipError_t launch_distill(const DistillArgs& a, hipStream_t stream) {
+hipError_t launch_distill(const DistillArgs& args, hipStream_t stream) {
+  DistillArgs a = args;
+  const double c = 1.4426950408889634 / (double)a.temperature;
+  a.inv = 1.f / a.temperature, a.c = (float)c, a.c_low = (float)(c - (double)a.c);
   if (a.dtype == TF_DT_F32) launch<TF_DT_F32>(a, stream);
   if (a.dtype == TF_DT_F16) launch<TF_DT_F16>(a, stream);
   if (a.dtype == TF_DT_BF16) launch<TF_DT_BF16>(a, stream);

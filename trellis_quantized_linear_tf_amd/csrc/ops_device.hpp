@@ -116,17 +116,62 @@ inline FastDiv fast_div(int d) {
   return {(uint32_t)(((1ull << (31 + s)) + (uint64_t)d - 1) / (uint64_t)d), 31 + s};
 }
 
+// Lane l's value from the lane that a DPP control word names; `rest` where it names none or
+// the row of 16 lanes is not in ROWS. A register move, where a shuffle is a trip to LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float v, float rest) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, rest), __builtin_bit_cast(int, v), CTRL,
+                                                               ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double v, double rest) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 a = __builtin_bit_cast(i32x2, v), r = __builtin_bit_cast(i32x2, rest);
+  const i32x2 d = {__builtin_amdgcn_update_dpp((int)r[0], (int)a[0], CTRL, ROWS, 0xF, false),
+                   __builtin_amdgcn_update_dpp((int)r[1], (int)a[1], CTRL, ROWS, 0xF, false)};
+  return __builtin_bit_cast(double, d);
+}
+
+constexpr int kShr = 0x110;      // + n: n lanes up within a row of 16
+constexpr int kBcast15 = 0x142;  // a row's last lane to the next row
+constexpr int kBcast31 = 0x143;  // lane 31 to the upper half
+
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 a = __builtin_bit_cast(i32x2, v);
+  const i32x2 d = {__builtin_amdgcn_readlane((int)a[0], lane), __builtin_amdgcn_readlane((int)a[1], lane)};
+  return __builtin_bit_cast(double, d);
+}
+
+// Running sum over the wave's lanes, each lane's own value in it.
 template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+__device__ __forceinline__ T wave_scan(T v) {
+  v += dpp<kShr + 1, 0xF>(v, (T)0);
+  v += dpp<kShr + 2, 0xF>(v, (T)0);
+  v += dpp<kShr + 4, 0xF>(v, (T)0);
+  v += dpp<kShr + 8, 0xF>(v, (T)0);
+  v += dpp<kBcast15, 0xA>(v, (T)0);
+  v += dpp<kBcast31, 0xC>(v, (T)0);
   return v;
 }
 
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+  return lane_of(wave_scan(v), 63);
+}
+
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  constexpr float none = -__builtin_inff();
+  v = fmaxf(v, dpp<kShr + 1, 0xF>(v, none));
+  v = fmaxf(v, dpp<kShr + 2, 0xF>(v, none));
+  v = fmaxf(v, dpp<kShr + 4, 0xF>(v, none));
+  v = fmaxf(v, dpp<kShr + 8, 0xF>(v, none));
+  v = fmaxf(v, dpp<kBcast15, 0xA>(v, none));
+  v = fmaxf(v, dpp<kBcast31, 0xC>(v, none));
+  return lane_of(v, 63);
 }
 
 // Sum and maximum over a workgroup of WAVES waves; every thread gets the result.

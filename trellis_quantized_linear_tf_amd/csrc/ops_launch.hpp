@@ -41,6 +41,7 @@ struct DistillArgs {
   int top_dtype;
   const float* weight;
   float temperature;
+  float inv, c, c_low;  // 1 / T; log2(e) / T in two parts
   float* loss;
   void* grad;
   int64_t grad_stride;

@@ -121,7 +121,8 @@ __device__ __forceinline__ bool find_run(ArgPtr x, int unit, Run* r) {
   const int lane = threadIdx.x & 63;
   int64_t all = 0;
   for (int b = lane; b < batch; b += 64) all += (cached(x, b) + nodes + KT - 1) / KT;
-  all = wave_sum(all);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
   const int64_t aim = (all + target - 1) / target;
   const int size = (int)(aim < x->p.min_tiles ? x->p.min_tiles : aim);
   int base = 0;

@@ -16,8 +16,9 @@ namespace tf_exl3 {
 constexpr int kLane = 32;           // logits of a chunk a lane
 constexpr int kChunk = 64 * kLane;  // 63.1 chunks of the head's 129280 columns: a lane each
 constexpr int kWaves = 4;           // waves of a workgroup of independent waves
-constexpr int kTreeWaves = 8;       // waves that share a sequence's rows
-constexpr int kMaxNodes = 1024;
+constexpr int kSampleThreads = 256;  // of the workgroup that looks through one chunk
+constexpr int kRun = kChunk / kSampleThreads;
+constexpr int kChainWaves = 8;
 
 struct ChunkStat {
   double sum;  // of exp((x - top) / T); not set at T <= 0
@@ -31,6 +32,8 @@ struct ChainEnd {
   float top;
   int row, first;
 };
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // 2^y for y <= 0 in 64 bits: 2^n 2^f with f = y - n in [-1/2, 1/2] and 2^f by the polynomial of
 // degree 10 that equals it at the eleven Chebyshev nodes of that range (3.1e-16 relative).
@@ -54,9 +57,9 @@ __device__ __forceinline__ double pow2_sum(double y) {
   y = fmax(y, -1000.0);
   const double t = y + 0x1.8p52;
   const double p = pow2_poly(y - (t - 0x1.8p52));
-  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
-  const uint32_t hi = (uint32_t)(bits >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | (uint32_t)bits);
+  u32x2 w = __builtin_bit_cast(u32x2, p);
+  w[1] += __builtin_bit_cast(u32x2, t)[0] << 20;
+  return __builtin_bit_cast(double, w);
 }
 
 // The weight of logit x in a row of maximum top, s = log2(e) / T; 0 where it underflows.
@@ -72,16 +75,23 @@ __device__ __forceinline__ double weight_of(float x, float top, double s) {
 __device__ __forceinline__ double log2_scale(float temperature) { return 1.4426950408889634 / (double)temperature; }
 __device__ __forceinline__ double fraction(float u) { return u > 0.f ? (double)u : 0.0; }
 
-// A chunk's logits, -inf for NaN and behind the row's end. RUNS: a lane has kLane
-// neighbours (for running sums); otherwise the lanes' pieces alternate.
-template <int DT, bool RUNS>
+// A wave's chunk, -inf behind the row's end; the lanes' pieces of 16 bytes alternate. Element
+// i of a lane stands at `place`.
+template <int DT>
+__device__ __forceinline__ int64_t place(int64_t at, int vocab, int i) {
+  constexpr int P = Elem<DT>::kPiece;
+  const int lane = threadIdx.x & 63;
+  return at + (at + kChunk <= vocab ? (i / P * 64 + lane) * P + i % P : i * 64 + lane);
+}
+
+template <int DT>
 __device__ __forceinline__ void load_chunk(const typename Elem<DT>::type* row, int64_t at, int vocab, float (&x)[kLane]) {
   constexpr int P = Elem<DT>::kPiece;
   const int lane = threadIdx.x & 63;
   if (at + kChunk <= vocab) {
     u32x4 v[kLane / P];
 #pragma unroll
-    for (int i = 0; i < kLane / P; ++i) v[i] = load_piece(row + at + (RUNS ? lane * kLane + i * P : (i * 64 + lane) * P));
+    for (int i = 0; i < kLane / P; ++i) v[i] = load_piece(row + at + (i * 64 + lane) * P);
 #pragma unroll
     for (int i = 0; i < kLane / P; ++i) {
       float e[P];
@@ -92,24 +102,29 @@ __device__ __forceinline__ void load_chunk(const typename Elem<DT>::type* row, i
   } else {
 #pragma unroll
     for (int i = 0; i < kLane; ++i) {
-      const int64_t j = at + (RUNS ? lane * kLane + i : i * 64 + lane);
+      const int64_t j = at + i * 64 + lane;
       x[i] = -INFINITY;
       if (j < vocab) x[i] = Elem<DT>::load(row[j]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kLane; ++i) x[i] = x[i] == x[i] ? x[i] : -INFINITY;
 }
 
-// Inclusive running sum over the wave's lanes.
-__device__ __forceinline__ double wave_scan(double v) {
-  const int lane = threadIdx.x & 63;
+// A thread's kRun neighbours of a workgroup's chunk, -inf behind the row's end.
+template <int DT>
+__device__ __forceinline__ void load_run(const typename Elem<DT>::type* row, int64_t at, int vocab, float (&x)[kRun]) {
+  constexpr int P = Elem<DT>::kPiece;
+  if (at + kRun <= vocab) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double up = __shfl_up(v, o);
-    if (lane >= o) v += up;
+    for (int i = 0; i < kRun / P; ++i) {
+      float e[P];
+      Elem<DT>::unpack(load_piece(row + at + i * P), e);
+#pragma unroll
+      for (int c = 0; c < P; ++c) x[i * P + c] = e[c];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) x[i] = at + i < vocab ? Elem<DT>::load(row[at + i]) : -INFINITY;
   }
-  return v;
 }
 
 template <int DT>
@@ -117,7 +132,7 @@ __device__ __forceinline__ const typename Elem<DT>::type* row_of(const VerifyArg
   return static_cast<const typename Elem<DT>::type*>(a.logits) + b * a.stride_batch + i * a.stride_node;
 }
 
-// One wave per chunk of every row. Bound by the fp64 rate: some 22 full-rate operations
+// One wave per chunk of every row. Bound by the fp64 rate: some 20 full-rate operations
 // a logit against 2 or 4 bytes.
 template <int DT>
 __global__ __launch_bounds__(kWaves * 64) void chunk_kernel(VerifyArgs a, int chunks) {
@@ -125,7 +140,7 @@ __global__ __launch_bounds__(kWaves * 64) void chunk_kernel(VerifyArgs a, int ch
   if (row >= (int64_t)a.batch * a.nodes) return;
   const int b = (int)(row / a.nodes), chunk = (int)(id - row * chunks);
   float x[kLane];
-  load_chunk<DT, false>(row_of<DT>(a, b, (int)(row - (int64_t)b * a.nodes)), (int64_t)chunk * kChunk, a.vocab, x);
+  load_chunk<DT>(row_of<DT>(a, b, (int)(row - (int64_t)b * a.nodes)), (int64_t)chunk * kChunk, a.vocab, x);
   float top = x[0];
 #pragma unroll
   for (int i = 1; i < kLane; ++i) top = fmaxf(top, x[i]);
@@ -133,18 +148,53 @@ __global__ __launch_bounds__(kWaves * 64) void chunk_kernel(VerifyArgs a, int ch
   const float t = a.temperature ? a.temperature[b] : 1.f;
   double sum = 0.0;
   if (t > 0.f && top > -INFINITY) {
-    double part[2] = {0.0, 0.0};
     if (top < INFINITY) {
       const double s = log2_scale(t), m = top;
+      sum = pow2_sum(((double)x[0] - m) * s);
 #pragma unroll
-      for (int i = 0; i < kLane; ++i) part[i & 1] += pow2_sum(((double)x[i] - m) * s);
+      for (int i = 1; i < kLane; ++i) sum += pow2_sum(((double)x[i] - m) * s);
     } else {
 #pragma unroll
-      for (int i = 0; i < kLane; ++i) part[i & 1] += x[i] == top ? 1.0 : 0.0;
+      for (int i = 0; i < kLane; ++i) sum += x[i] == top ? 1.0 : 0.0;
     }
-    sum = wave_sum(part[0] + part[1]);
+    sum = wave_sum(sum);
   }
   if ((threadIdx.x & 63) == 0) static_cast<ChunkStat*>(a.workspace)[id] = {sum, top, 0};
+}
+
+// Where the running sum of part(c) over a row's chunks first is over u times its total; at
+// the last chunk of any weight if rounding lets none be. One wave, or each of several.
+struct Cross {
+  int chunk;  // -1: no weight at all
+  double before, goal;
+};
+
+template <typename F>
+__device__ __forceinline__ Cross cross_chunk(int chunks, double u, F part) {
+  const int lane = threadIdx.x & 63;
+  double base = 0.0, v = 0.0, run = 0.0;
+  for (int c0 = 0; c0 < chunks; c0 += 64) {
+    v = c0 + lane < chunks ? part(c0 + lane) : 0.0;
+    run = base + wave_scan(v);
+    base = lane_of(run, 63);
+  }
+  Cross x = {-1, 0.0, u * base};
+  base = 0.0;
+  for (int c0 = 0; c0 < chunks; c0 += 64) {
+    if (chunks > 64) {  // otherwise at hand
+      v = c0 + lane < chunks ? part(c0 + lane) : 0.0;
+      run = base + wave_scan(v);
+    }
+    const uint64_t over = __ballot(v > 0.0 && run > x.goal), any = __ballot(v > 0.0);
+    if (any) {
+      const int at = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(any);
+      x.chunk = c0 + at;
+      x.before = at > 0 ? lane_of(run, at - 1) : base;
+      if (over) break;
+    }
+    base = lane_of(run, 63);
+  }
+  return x;
 }
 
 __device__ __forceinline__ float row_top(const ChunkStat* stat, int chunks) {
@@ -153,123 +203,109 @@ __device__ __forceinline__ float row_top(const ChunkStat* stat, int chunks) {
   return wave_max(top);
 }
 
-__device__ __forceinline__ double row_sum(const ChunkStat* stat, int chunks, float top, double s) {
-  double z = 0.0;
-  for (int c = threadIdx.x & 63; c < chunks; c += 64) z += stat[c].sum * weight_of(stat[c].top, top, s);
-  return wave_sum(z);
-}
-
-// First place of a row's maximum; top is above -inf.
-template <int DT>
-__device__ int first_place(const typename Elem<DT>::type* row, const ChunkStat* stat, int chunks, int vocab, float top) {
+// First chunk of a row that holds its maximum.
+__device__ __forceinline__ int top_chunk(const ChunkStat* stat, int chunks, float top) {
   const int lane = threadIdx.x & 63;
-  int chunk = 0;
   for (int c0 = 0; c0 < chunks; c0 += 64) {
     const uint64_t hit = __ballot(c0 + lane < chunks && stat[c0 + lane < chunks ? c0 + lane : 0].top == top);
-    if (hit) {
-      chunk = c0 + __builtin_ctzll(hit);
-      break;
-    }
+    if (hit) return c0 + __builtin_ctzll(hit);
   }
-  float x[kLane];
-  load_chunk<DT, true>(row, (int64_t)chunk * kChunk, vocab, x);
-  int mine = kLane;
-#pragma unroll
-  for (int i = kLane - 1; i >= 0; --i) mine = x[i] == top ? i : mine;
-  const uint64_t hit = __ballot(mine < kLane);
-  const int at = hit ? __builtin_ctzll(hit) : 0;
-  return chunk * kChunk + at * kLane + __shfl(mine, at);
+  return 0;
 }
 
-// Where the running sum of part(c), over the chunks c of a row, first is over goal: the
-// chunk, and the sum before it. The last chunk of any weight where rounding lets none be.
-template <typename F>
-__device__ __forceinline__ int cross_chunk(int chunks, double goal, F part, double* before) {
-  const int lane = threadIdx.x & 63;
-  double base = 0.0, held = 0.0;
-  int last = -1;
-  for (int c0 = 0; c0 < chunks; c0 += 64) {
-    const double v = c0 + lane < chunks ? part(c0 + lane) : 0.0;
-    const double run = base + wave_scan(v);
-    const uint64_t over = __ballot(v > 0.0 && run > goal), any = __ballot(v > 0.0);
-    if (any) {
-      const int at = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(any);
-      const double up = __shfl(run, at > 0 ? at - 1 : 0);
-      last = c0 + at;
-      held = at > 0 ? up : base;
-      if (over) break;
-    }
-    base = __shfl(run, 63);
-  }
-  *before = held;
-  return last;
-}
+struct Found {
+  double sum[kSampleThreads / 64];
+  int first[kSampleThreads / 64], last[kSampleThreads / 64];
+};
 
-// The place in a chunk whose running sum, begun at before, first is over goal; the last
-// place of any weight where rounding lets none be. w: the weights of the lane's run.
-__device__ __forceinline__ int cross_place(const double (&w)[kLane], double before, double goal) {
+// The place in a workgroup's chunk, whose threads hold the weights w of their runs, where
+// the running sum, begun at before, first is over goal; the last place of any weight if
+// rounding lets none be.
+__device__ __forceinline__ int cross_place(const double (&w)[kRun], double before, double goal, Found& f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double mine = 0.0;
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) mine += w[i];
-  const double run = before + wave_scan(mine);
-  const uint64_t over = __ballot(mine > 0.0 && run > goal), any = __ballot(mine > 0.0);
-  const int at = over ? __builtin_ctzll(over) : any ? 63 - __builtin_clzll(any) : 0;
-  double c = __shfl_up(run, 1);
-  if ((threadIdx.x & 63) == 0) c = before;
-  int place = -1, last = 0;
+  for (int i = 0; i < kRun; ++i) mine += w[i];
+  const double scan = wave_scan(mine);
+  if (lane == 63) f.sum[wave] = scan;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) before += f.sum[i];
+  const double run = before + scan;
+  double c = run - mine;
+  int over = kRun, last = 0;
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) {
+  for (int i = 0; i < kRun; ++i) {
     c += w[i];
     if (w[i] > 0.0) {
       last = i;
-      if (place < 0 && c > goal) place = i;
+      if (over == kRun && c > goal) over = i;
     }
   }
-  return at * kLane + __shfl(place < 0 ? last : place, at);
+  const uint64_t hit = __ballot(mine > 0.0 && run > goal), any = __ballot(mine > 0.0);
+  if (lane == 0) f.first[wave] = f.last[wave] = -1;
+  const int from = threadIdx.x * kRun;
+  if (hit && lane == __builtin_ctzll(hit)) f.first[wave] = from + (over < kRun ? over : last);
+  if (any && lane == 63 - __builtin_clzll(any)) f.last[wave] = from + last;
+  __syncthreads();
+  int at = 0;
+  for (int i = 0; i < kSampleThreads / 64; ++i)
+    if (f.last[i] >= 0) at = f.last[i];
+  for (int i = kSampleThreads / 64 - 1; i >= 0; --i)
+    if (f.first[i] >= 0) at = f.first[i];
+  return at;
 }
 
-// A row's token, from its chunks; one wave, every lane gets it.
+// A row's token from its chunks; one workgroup, every thread gets it.
 template <int DT>
-__device__ int sample_row(const typename Elem<DT>::type* row, const ChunkStat* stat, int chunks, int vocab, float t, float u) {
+__device__ __forceinline__ int sample_row(const typename Elem<DT>::type* row, const ChunkStat* stat, int chunks, int vocab, float t,
+                                          float u, Found& f) {
   const float top = row_top(stat, chunks);
   if (top == -INFINITY) return -1;
-  if (!(t > 0.f)) return first_place<DT>(row, stat, chunks, vocab, top);
-  const double s = log2_scale(t);
-  double before;
-  const double goal = fraction(u) * row_sum(stat, chunks, top, s);
-  const int chunk = cross_chunk(chunks, goal, [&](int c) { return stat[c].sum * weight_of(stat[c].top, top, s); }, &before);
-  float x[kLane];
-  load_chunk<DT, true>(row, (int64_t)chunk * kChunk, vocab, x);
-  double w[kLane];
+  float x[kRun];
+  double w[kRun];
+  Cross at = {0, 0.0, 0.0};
+  if (t > 0.f) {
+    const double s = log2_scale(t);
+    at = cross_chunk(chunks, fraction(u), [&](int c) { return stat[c].sum * weight_of(stat[c].top, top, s); });
+    load_run<DT>(row, (int64_t)at.chunk * kChunk + threadIdx.x * kRun, vocab, x);
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) w[i] = weight_of(x[i], top, s);
-  return chunk * kChunk + cross_place(w, before, goal);
+    for (int i = 0; i < kRun; ++i) w[i] = weight_of(x[i], top, s);
+  } else {
+    at.chunk = top_chunk(stat, chunks, top);
+    load_run<DT>(row, (int64_t)at.chunk * kChunk + threadIdx.x * kRun, vocab, x);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) w[i] = x[i] == top ? 1.0 : 0.0;
+  }
+  return at.chunk * kChunk + cross_place(w, at.before, at.goal, f);
 }
 
-// One workgroup per sequence: its rows' tokens, a wave a row, then the first wave's walk.
+// One workgroup per row: its token.
 template <int DT>
-__global__ __launch_bounds__(kTreeWaves * 64) void tree_kernel(VerifyArgs a, int chunks) {
-  __shared__ int token[kMaxNodes];
-  const int b = blockIdx.x, lane = threadIdx.x & 63;
+__global__ __launch_bounds__(kSampleThreads) void token_kernel(VerifyArgs a, int chunks, int32_t* token) {
+  __shared__ Found f;
+  const int64_t row = blockIdx.x;
+  const int b = (int)(row / a.nodes), i = (int)(row - (int64_t)b * a.nodes);
+  const int got = sample_row<DT>(row_of<DT>(a, b, i), static_cast<const ChunkStat*>(a.workspace) + row * chunks, chunks, a.vocab,
+                                 a.temperature ? a.temperature[b] : 1.f, a.u[row], f);
+  if (threadIdx.x == 0) token[row] = got;
+}
+
+// One wave per sequence walks its tree, 64 nodes looked at together.
+__global__ __launch_bounds__(64) void walk_kernel(VerifyArgs a, const int32_t* token) {
+  const int b = blockIdx.x, lane = threadIdx.x;
   const int64_t at = (int64_t)b * a.nodes;
-  const float t = a.temperature ? a.temperature[b] : 1.f;
-  const ChunkStat* stat = static_cast<const ChunkStat*>(a.workspace) + at * chunks;
-  for (int i = threadIdx.x >> 6; i < a.nodes; i += kTreeWaves) {
-    const int got = sample_row<DT>(row_of<DT>(a, b, i), stat + (int64_t)i * chunks, chunks, a.vocab, t, a.u[at + i]);
-    if (lane == 0) token[i] = got;
-  }
-  __syncthreads();
-  if (threadIdx.x >= 64) return;
+  int parent = -1, mine = -1, row_token = -1;  // of node `lane`, for trees of up to 64
+  if (lane < a.nodes) parent = a.parents[at + lane], mine = a.tokens[at + lane], row_token = token[at + lane];
   int node = 0, count = 0;
   while (node >= 0) {
     if (lane == 0) a.accepted[at + count] = node;
     ++count;
-    const int want = token[node];
+    const int want = node < 64 ? __builtin_amdgcn_readlane(row_token, node) : token[at + node];
     int next = -1;
     for (int c0 = node / 64 * 64; c0 < a.nodes && next < 0; c0 += 64) {
-      const int c = c0 + lane;
-      const uint64_t hit = __ballot(c > node && c < a.nodes && want >= 0 && a.parents[at + (c < a.nodes ? c : 0)] == node &&
-                                    a.tokens[at + (c < a.nodes ? c : 0)] == want);
+      const int c = c0 + lane, have = c < a.nodes ? c : 0;
+      const bool child = c0 == 0 ? parent == node && mine == want : a.parents[at + have] == node && a.tokens[at + have] == want;
+      const uint64_t hit = __ballot(c > node && c < a.nodes && want >= 0 && child);
       if (hit) next = c0 + __builtin_ctzll(hit);
     }
     if (next < 0 && lane == 0) {
@@ -287,71 +323,71 @@ struct Row {
   double z;
 };
 
+// A row's maximum with its sum or, at T <= 0, its first place; one wave.
 template <int DT>
 __device__ __forceinline__ Row row_stat(const VerifyArgs& a, int chunks, int b, int j, float t) {
   const ChunkStat* stat = static_cast<const ChunkStat*>(a.workspace) + ((int64_t)b * a.nodes + j) * chunks;
   Row r = {row_top(stat, chunks), -1, 0.0};
   if (r.top == -INFINITY) return r;
   if (t > 0.f) {
-    r.z = row_sum(stat, chunks, r.top, log2_scale(t));
+    const double s = log2_scale(t);
+    double z = 0.0;
+    for (int c = threadIdx.x & 63; c < chunks; c += 64) z += stat[c].sum * weight_of(stat[c].top, r.top, s);
+    r.z = wave_sum(z);
   } else {
-    r.first = first_place<DT>(row_of<DT>(a, b, j), stat, chunks, a.vocab, r.top);
+    const int64_t at = (int64_t)top_chunk(stat, chunks, r.top) * kChunk;
+    float x[kLane];
+    load_chunk<DT>(row_of<DT>(a, b, j), at, a.vocab, x);
+    int64_t first = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = kLane - 1; i >= 0; --i) first = x[i] == r.top ? place<DT>(at, a.vocab, i) : first;
+    int low = (int)first;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) low = min(low, __shfl_xor(low, o));
+    r.first = low;
     r.z = 1.0;
   }
   return r;
 }
 
-// Probability of place i with logit x; s is not used at T <= 0.
+// Probability of place i with logit x; s = log2(e) / T, not used at T <= 0.
 __device__ __forceinline__ double probability(const Row& r, float t, double s, int i, float x) {
   if (!(t > 0.f)) return i == r.first ? 1.0 : 0.0;
-  return r.z > 0.0 ? weight_of(x == x ? x : -INFINITY, r.top, s) / r.z : 0.0;
+  return r.z > 0.0 ? weight_of(x, r.top, s) / r.z : 0.0;
 }
 
-// max(p - q, 0) of the lane's part of a chunk (p where q is NULL).
-template <int DT, bool RUNS>
-__device__ __forceinline__ void residual(const typename Elem<DT>::type* row, const float* q, const Row& r, float t, int64_t at,
-                                         int vocab, double (&w)[kLane]) {
-  constexpr int P = Elem<DT>::kPiece;
-  const int lane = threadIdx.x & 63;
-  const double s = t > 0.f ? log2_scale(t) : 0.0;
-  const bool whole = at + kChunk <= vocab;  // as load_chunk goes
-  float x[kLane];
-  load_chunk<DT, RUNS>(row, at, vocab, x);
-#pragma unroll
-  for (int i = 0; i < kLane; ++i) {
-    const int64_t j = at + (RUNS ? lane * kLane + i : whole ? (i / P * 64 + lane) * P + i % P : i * 64 + lane);
-    double p = probability(r, t, s, (int)j, x[i]);
-    if (q != nullptr && j < vocab) p -= (double)q[j];
-    w[i] = p > 0.0 && j < vocab ? p : 0.0;
-  }
+// The same by the reciprocal of the sum, for residuals: where p and q, which has 24 bits, can
+// be equal at all (a power of two) the product is as exact as the quotient.
+__device__ __forceinline__ double residual(const Row& r, double s, double inv, float x, float q) {
+  const double d = weight_of(x, r.top, s) * inv - (double)q;
+  return d > 0.0 ? d : 0.0;
 }
 
 // One workgroup per sequence and group of chunks: goes down the drafts to the first that
-// is refused, then sums max(p - q, 0) over its chunks of that row, a wave each. Every
-// workgroup of a sequence takes the same way.
+// is refused, a wave a row, then sums max(p - q, 0) over its chunks of that row, a wave each.
+// Every workgroup of a sequence takes the same way. At T <= 0 there is nothing to sum: p
+// is 1 at one place, which is the token whatever q holds.
 template <int DT>
-__global__ __launch_bounds__(kWaves * 64) void chain_kernel(VerifyArgs a, int chunks, double* sums, ChainEnd* ends) {
-  __shared__ int refused[kWaves];
-  __shared__ Row rows[kWaves];
+__global__ __launch_bounds__(kChainWaves * 64) void chain_kernel(VerifyArgs a, int chunks, double* sums, ChainEnd* ends) {
+  __shared__ int refused[kChainWaves];
+  __shared__ Row rows[kChainWaves];
   const int b = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t at = (int64_t)b * a.nodes;
   const float t = a.temperature ? a.temperature[b] : 1.f;
+  const double s = t > 0.f ? log2_scale(t) : 0.0;
   int stop = -1;
-  for (int j0 = 0; stop < 0; j0 += kWaves) {
+  for (int j0 = 0; stop < 0; j0 += kChainWaves) {
     const int j = j0 + wave;
     int no = 0;
     Row r = {-INFINITY, -1, 0.0};
     if (j < a.nodes) {
-      r = row_stat<DT>(a, chunks, b, j, t);
       no = 1;  // the last row has no draft
-      if (j + 1 < a.nodes) {
-        const int x = a.tokens[at + j + 1];
-        if (x >= 0 && x < a.vocab) {
-          const double p = probability(r, t, t > 0.f ? log2_scale(t) : 0.0, x, Elem<DT>::load(row_of<DT>(a, b, j)[x]));
-          const float q = a.q[b * a.q_stride_batch + j * a.q_stride_node + x];
-          no = !(fraction(a.u[at + j]) * (double)q < p);
-        }
-      }
+      const int x = j + 1 < a.nodes ? a.tokens[at + j + 1] : -1;
+      const bool draft = x >= 0 && x < a.vocab;
+      const float logit = draft ? Elem<DT>::load(row_of<DT>(a, b, j)[x]) : 0.f;
+      const float q = draft ? a.q[b * a.q_stride_batch + j * a.q_stride_node + x] : 0.f;
+      r = row_stat<DT>(a, chunks, b, j, t);
+      if (draft) no = !(fraction(a.u[at + j]) * (double)q < probability(r, t, s, x, logit));
     }
     __syncthreads();
     if (lane == 0) {
@@ -359,48 +395,79 @@ __global__ __launch_bounds__(kWaves * 64) void chain_kernel(VerifyArgs a, int ch
       rows[wave] = r;
     }
     __syncthreads();
-    for (int w = kWaves - 1; w >= 0; --w)
+    for (int w = kChainWaves - 1; w >= 0; --w)
       if (refused[w]) stop = j0 + w;
   }
-  const Row r = rows[stop % kWaves];
-  const int chunk = blockIdx.x * kWaves + wave;
+  const Row r = rows[stop % kChainWaves];
+  const int chunk = blockIdx.x * kChainWaves + wave;
   if (blockIdx.x == 0 && threadIdx.x == 0) ends[b] = {r.z, r.top, stop, r.first};
-  if (chunk >= chunks || stop + 1 == a.nodes) return;
-  double w[kLane], sum = 0.0;
-  residual<DT, false>(row_of<DT>(a, b, stop), a.q + b * a.q_stride_batch + stop * a.q_stride_node, r, t,
-                      (int64_t)chunk * kChunk, a.vocab, w);
+  if (chunk >= chunks || stop + 1 == a.nodes || !(t > 0.f)) return;
+  const int64_t from = (int64_t)chunk * kChunk;
+  const float* q = a.q + b * a.q_stride_batch + stop * a.q_stride_node;
+  const auto* row = row_of<DT>(a, b, stop);
+  const double inv = r.z > 0.0 ? 1.0 / r.z : 0.0;
+  double sum = 0.0;
+  if (from + kChunk <= a.vocab && r.top < INFINITY) {
+    constexpr int P = Elem<DT>::kPiece;
+    const double m = r.top;
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) sum += w[i];
+    for (int i = 0; i < kLane; i += P) {
+      const int64_t j = place<DT>(from, a.vocab, i);
+      float x[P];
+      Elem<DT>::unpack(load_piece(row + j), x);
+#pragma unroll
+      for (int h = 0; h < P; h += 4) {
+        const u32x4 v = load_piece(q + j + h);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const double y = ((double)x[h + c] - m) * s, w = y > -1000.0 ? pow2_sum(y) : 0.0;
+          const double d = w * inv - (double)bits_to_f32(v[c]);
+          sum += d > 0.0 ? d : 0.0;
+        }
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int64_t j = from + lane; j < from + kChunk && j < a.vocab; j += 64)
+      sum += residual(r, s, inv, Elem<DT>::load(row[j]), q[j]);
+  }
   sum = wave_sum(sum);
   if (lane == 0) sums[(int64_t)b * chunks + chunk] = sum;
 }
 
-// One wave per sequence: the token after the accepted drafts.
+// One workgroup per sequence: the token after the accepted drafts.
 template <int DT>
-__global__ __launch_bounds__(64) void chain_next_kernel(VerifyArgs a, int chunks, const double* sums, const ChainEnd* ends) {
-  const int b = blockIdx.x, lane = threadIdx.x;
+__global__ __launch_bounds__(kSampleThreads) void chain_next_kernel(VerifyArgs a, int chunks, const double* sums,
+                                                                    const ChainEnd* ends) {
+  __shared__ Found f;
+  const int b = blockIdx.x;
   const ChainEnd end = ends[b];
   const float t = a.temperature ? a.temperature[b] : 1.f, u = a.u[(int64_t)b * a.nodes + a.nodes - 1];
   const auto* row = row_of<DT>(a, b, end.row);
-  double total = 0.0;
-  if (end.row + 1 < a.nodes)
-    for (int c = lane; c < chunks; c += 64) total += sums[(int64_t)b * chunks + c];
-  total = wave_sum(total);
-  int place;
-  if (total > 0.0) {
-    double before, w[kLane];
-    const double goal = fraction(u) * total;
-    const int chunk = cross_chunk(chunks, goal, [&](int c) { return sums[(int64_t)b * chunks + c]; }, &before);
-    residual<DT, true>(row, a.q + b * a.q_stride_batch + end.row * a.q_stride_node, {end.top, end.first, end.z}, t,
-                       (int64_t)chunk * kChunk, a.vocab, w);
-    place = chunk * kChunk + cross_place(w, before, goal);
+  Cross at = {-1, 0.0, 0.0};
+  if (end.row + 1 < a.nodes && t > 0.f) at = cross_chunk(chunks, fraction(u), [&](int c) { return sums[(int64_t)b * chunks + c]; });
+  int token;
+  if (!(t > 0.f)) {
+    token = end.first;
+  } else if (at.chunk >= 0) {
+    const Row r = {end.top, end.first, end.z};
+    const double s = log2_scale(t), inv = r.z > 0.0 ? 1.0 / r.z : 0.0;
+    const float* q = a.q + b * a.q_stride_batch + end.row * a.q_stride_node;
+    const int64_t from = (int64_t)at.chunk * kChunk + threadIdx.x * kRun;
+    float x[kRun], qx[kRun];
+    double w[kRun];
+    load_run<DT>(row, from, a.vocab, x);
+    load_run<TF_DT_F32>(q, from, a.vocab, qx);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) w[i] = from + i < a.vocab ? residual(r, s, inv, x[i], qx[i]) : 0.0;
+    token = at.chunk * kChunk + cross_place(w, at.before, at.goal, f);
   } else {
     const ChunkStat* stat = static_cast<const ChunkStat*>(a.workspace) + ((int64_t)b * a.nodes + end.row) * chunks;
-    place = sample_row<DT>(row, stat, chunks, a.vocab, t, u);
+    token = sample_row<DT>(row, stat, chunks, a.vocab, t, u, f);
   }
-  if (lane == 0) {
+  if (threadIdx.x == 0) {
     a.count[b] = end.row + 1;
-    a.next[b] = place;
+    a.next[b] = token;
   }
 }
 
@@ -413,20 +480,23 @@ static hipError_t launch(const VerifyArgs& a, hipStream_t stream) {
   if (groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(chunk_kernel<DT>, dim3((unsigned)groups), dim3(kWaves * 64), 0, stream, a, chunks);
   if (a.parents != nullptr) {
-    hipLaunchKernelGGL(tree_kernel<DT>, dim3(a.batch), dim3(kTreeWaves * 64), 0, stream, a, chunks);
+    int32_t* token = reinterpret_cast<int32_t*>(static_cast<ChunkStat*>(a.workspace) + rows * chunks);
+    hipLaunchKernelGGL(token_kernel<DT>, dim3((unsigned)rows), dim3(kSampleThreads), 0, stream, a, chunks, token);
+    hipLaunchKernelGGL(walk_kernel, dim3(a.batch), dim3(64), 0, stream, a, token);
   } else {
     double* sums = reinterpret_cast<double*>(static_cast<ChunkStat*>(a.workspace) + rows * chunks);
     ChainEnd* ends = reinterpret_cast<ChainEnd*>(sums + (int64_t)a.batch * chunks);
-    hipLaunchKernelGGL(chain_kernel<DT>, dim3((chunks + kWaves - 1) / kWaves, a.batch), dim3(kWaves * 64), 0, stream, a, chunks,
-                       sums, ends);
-    hipLaunchKernelGGL(chain_next_kernel<DT>, dim3(a.batch), dim3(64), 0, stream, a, chunks, sums, ends);
+    hipLaunchKernelGGL(chain_kernel<DT>, dim3((chunks + kChainWaves - 1) / kChainWaves, a.batch), dim3(kChainWaves * 64), 0, stream,
+                       a, chunks, sums, ends);
+    hipLaunchKernelGGL(chain_next_kernel<DT>, dim3(a.batch), dim3(kSampleThreads), 0, stream, a, chunks, sums, ends);
   }
   return hipGetLastError();
 }
 
 size_t verify_workspace(int batch, int nodes, int vocab) {
   const size_t chunks = (size_t)chunks_of(vocab), b = (size_t)(batch < 1 ? 1 : batch);
-  return (b * nodes * chunks * sizeof(ChunkStat) + b * chunks * sizeof(double) + b * sizeof(ChainEnd) + 15) / 16 * 16;
+  const size_t tree = b * nodes * sizeof(int32_t), chain = b * (chunks * sizeof(double) + sizeof(ChainEnd));
+  return (b * nodes * chunks * sizeof(ChunkStat) + (tree > chain ? tree : chain) + 15) / 16 * 16;
 }
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream) {
