@@ -65,9 +65,8 @@ __device__ __forceinline__ void take(const u32x4* v, const Scale& sc, float& m, 
 // the thread that writes the piece with its place, so each thread has a list of its entries.
 template <int THREADS>
 struct Teacher {
-  float t[kMaxTop + 8];  // probability; eight left out entries stand behind the last
-  int at[kMaxTop + 8];   // place, -1 for an entry that is left out
-  float all[kMaxTop];    // sum of the probabilities at its place
+  float t[kMaxTop];  // probability
+  int at[kMaxTop];   // place, -1 for an entry that is left out
   int next[kMaxTop], head[THREADS];
   int none;  // no entry at all
 };
@@ -107,7 +106,6 @@ struct Entries {
       any = any || at >= 0;
       ymax = fmaxf(ymax, s.t[j]);
     }
-    if (lane < 8) s.at[a.top_k + lane] = -1, s.t[a.top_k + lane] = 0.f;
     ymax = wave_max(lane < a.top_k ? ymax : -INFINITY);
     const uint64_t some = __ballot(any);
     if (lane == 0) s.none = some == 0;
@@ -134,30 +132,19 @@ struct Entries {
   }
 };
 
-// Entries with places in the pieces [lo, hi), each place once, into the lists of the threads
-// that write them: the piece's number modulo THREADS, or a row's last elements in order.
+// Entries with places in the pieces [lo, hi) into the lists of the threads that write them:
+// the piece's number modulo THREADS, or a row's last elements in order. What is made of a
+// list does not depend on its order.
 template <int P, int THREADS>
 __device__ __forceinline__ void link(const DistillArgs& a, Teacher<THREADS>& s, int pieces, int64_t lo, int64_t hi) {
   for (int j = threadIdx.x; j < a.top_k; j += THREADS) {
     const int at = s.at[j], piece = at / P;
     if (at < 0 || piece < lo || piece >= hi) continue;
-    float t = 0.f;
-    bool first = true;
-    for (int i0 = 0; i0 < a.top_k; i0 += 8) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool same = s.at[i0 + i] == at;
-        first = first && !(same && i0 + i < j);
-        t += same ? s.t[i0 + i] : 0.f;
-      }
-    }
-    if (!first) continue;
-    s.all[j] = t;
     s.next[j] = atomicExch(&s.head[piece < pieces ? piece % THREADS : at - pieces * P], j);
   }
 }
 
-// What a thread writes of a row's gradient.
+// What a thread writes of a row's gradient. Its pieces are numbered by `slot`.
 template <int DT, int THREADS>
 struct Writer {
   static constexpr int P = Elem<DT>::kPiece;
@@ -165,39 +152,58 @@ struct Writer {
   const Teacher<THREADS>& s;
   float top, z, w, w_z;
   bool zero;
-  int piece, at, next;  // of the list's first entry
+  int first, at, next;  // the list's first entry
   float t;
+  uint32_t slots;  // with an entry; 31 stands for all from 31 on
 
-  __device__ __forceinline__ Writer(const Scale& scale, const Teacher<THREADS>& teach, float top_, float z_, float weight)
+  __device__ __forceinline__ Writer(const Scale& scale, const Teacher<THREADS>& teach, float top_, float z_, float weight, int64_t lo)
       : sc(scale), s(teach), top(top_), z(z_), w(teach.none ? 0.f : weight * scale.inv), w_z(w / z_), zero(w == 0.f) {
-    const int j = s.head[threadIdx.x];
-    piece = at = next = -1, t = 0.f;
-    if (j >= 0) at = s.at[j], piece = at / P, t = s.all[j], next = s.next[j];
+    first = s.head[threadIdx.x], at = next = -1, t = 0.f, slots = 0;
+    if (first >= 0) at = s.at[first], t = s.t[first], next = s.next[first];
+    for (int j = first; j >= 0; j = s.next[j]) slots |= 1u << slot_of((int)((s.at[j] / P - lo) / THREADS));
   }
-  __device__ __forceinline__ void fix(const float (&x)[P], float (&g)[P], int at, float t) const {
+  __device__ static __forceinline__ int slot_of(int i) { return i < 31 ? i : 31; }
+
+  // The teacher's mass at a place of the list: the sum of two does not depend on their order,
+  // that of more is taken in units of 2^-62.
+  __device__ __forceinline__ float mass(int place) const {
+    float sum = 0.f;
+    uint64_t units = 0;
+    int n = 0;
+    for (int j = first; j >= 0; j = s.next[j])
+      if (s.at[j] == place) {
+        sum += s.t[j];
+        units += (uint64_t)((double)s.t[j] * 0x1p62);
+        ++n;
+      }
+    return n > 2 && sum == sum ? (float)((double)units * 0x1p-62) : sum;
+  }
+  __device__ __forceinline__ float at_place(float x, float mass) const { return (sc.exp(x - top) / z - mass) * w; }
+  __device__ __forceinline__ void fix(const float (&x)[P], float (&g)[P], int c, float mass) const {
 #pragma unroll
-    for (int c = 0; c < P; ++c)
-      if (at % P == c) g[c] = (sc.exp(x[c] - top) / z - t) * w;
+    for (int i = 0; i < P; ++i)
+      if (i == c) g[i] = at_place(x[i], mass);
   }
-  __device__ __forceinline__ u32x4 operator()(u32x4 v, int64_t p) const {
+  __device__ __forceinline__ u32x4 operator()(u32x4 v, int64_t p, int slot) const {
     if (zero) return u32x4(0u);  // whatever the row holds
     float x[P], g[P];
     Elem<DT>::unpack(v, x);
 #pragma unroll
     for (int c = 0; c < P; ++c) g[c] = sc.exp(x[c] - top) * w_z;
-    if (p == piece) fix(x, g, at, t);
-    if (next >= 0) {  // seldom
-      for (int j = next; j >= 0; j = s.next[j])
-        if (p == s.at[j] / P) fix(x, g, s.at[j], s.all[j]);
+    if ((slots >> slot_of(slot)) & 1) {
+      if (next < 0) {
+        if (at / P == p) fix(x, g, at % P, t);
+      } else {
+        for (int j = first; j >= 0; j = s.next[j])
+          if (s.at[j] / P == p) fix(x, g, s.at[j] % P, mass(s.at[j]));
+      }
     }
     return Elem<DT>::pack(g);
   }
-  __device__ __forceinline__ typename Elem<DT>::type last(float x, int pieces) const {
+  // The thread's element behind the whole pieces, at `place`.
+  __device__ __forceinline__ typename Elem<DT>::type last(float x, int64_t place) const {
     if (zero) return Elem<DT>::store(0.f);
-    float total = piece == pieces ? t : 0.f;
-    for (int j = next; j >= 0; j = s.next[j])
-      if (s.at[j] / P == pieces) total = s.all[j];
-    return Elem<DT>::store((sc.exp(x - top) / z - total) * w);
+    return Elem<DT>::store(at_place(x, mass((int)place)));
   }
 };
 
@@ -256,15 +262,15 @@ __global__ __launch_bounds__(THREADS, 4) void distill_row_kernel(DistillArgs a) 
   if (!a.grad) return;
 
   T* grad = static_cast<T*>(a.grad) + r * a.grad_stride;
-  const Writer<DT, THREADS> out(sc, teach, top, z, a.weight[r]);
+  const Writer<DT, THREADS> out(sc, teach, top, z, a.weight[r], 0);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int p = i * THREADS + tid;
-    if (p < pieces) store_piece(grad + (int64_t)p * P, out(v[i], p));
+    if (p < pieces) store_piece(grad + (int64_t)p * P, out(v[i], p, i));
   }
-  if (tid < rest) grad[(int64_t)pieces * P + tid] = out.last(last, pieces);
+  if (tid < rest) grad[(int64_t)pieces * P + tid] = out.last(last, (int64_t)pieces * P + tid);
   for (int i = N * THREADS + tid; i < pieces; i += THREADS)
-    store_piece(grad + (int64_t)i * P, out(load_piece(x + (int64_t)i * P), i));
+    store_piece(grad + (int64_t)i * P, out(load_piece(x + (int64_t)i * P), i, i / THREADS));
 }
 
 // Few rows: each is cut into parts of kPart pieces, one workgroup each. The first launch
@@ -352,14 +358,14 @@ __global__ __launch_bounds__(kPartThreads) void distill_join_kernel(DistillArgs 
   if (!a.grad) return;
 
   T* grad = static_cast<T*>(a.grad) + r * a.grad_stride;
-  const Writer<DT, kPartThreads> out(sc, teach, top, z, a.weight[r]);
+  const Writer<DT, kPartThreads> out(sc, teach, top, z, a.weight[r], lo);
 #pragma unroll
   for (int i = 0; i < kPartPieces; ++i) {
     const int64_t p = lo + i * kPartThreads + tid;
-    if (p < pieces) store_piece(grad + p * P, out(v[i], p));
+    if (p < pieces) store_piece(grad + p * P, out(v[i], p, i));
   }
   const int64_t at = (int64_t)pieces * P + tid;
-  if (part == 0 && at < a.vocab) grad[at] = out.last(last, pieces);
+  if (part == 0 && at < a.vocab) grad[at] = out.last(last, at);
 }
 
 static int parts_of(int dtype, int vocab) {
