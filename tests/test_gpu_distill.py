@@ -64,7 +64,7 @@ def check(x, index, top, w, temperature=1.0, got=None):
     scale = (np.abs(w64) / temperature)[:, None]
     h = torch.finfo(x.dtype).eps / 2
     dx = top_x - xs
-    dp = p * (4 * dx + n + 16) * F
+    dp = np.where(p > 0, p * (4 * np.where(p > 0, dx, 0) + n + 16) * F, 0.0)  # -inf has exactly no probability
     dt_ = t * (4 * ry.max(1, keepdims=True) + n + 16 + index.shape[1]) * F
     tol = scale * (dp + dt_ + 4 * F * (p + t)) * (1 + h) + h * np.abs(want_grad)
     tol += {"torch.float16": 2.0 ** -24, "torch.bfloat16": 2.0 ** -126, "torch.float32": 2.0 ** -126}[str(x.dtype)]
@@ -87,6 +87,17 @@ def test_vocabularies(gpu, dt, vocab):
 def test_entries_and_temperatures(gpu, k, temperature):
     say(f"entries {k} at {temperature}")
     check(*inputs(k, 4, 3001, k, "bf16", "f32"), temperature)
+
+
+@pytest.mark.parametrize("temperature", [0.1, 0.3, 0.7, 1.3, 3.0, 7.0, 1.4426950216293335])
+@pytest.mark.parametrize("rows,vocab", [(3, 777), (3, 20011), (200, 20011)])
+def test_temperatures_that_round_either_way(gpu, temperature, rows, vocab):
+    """log2(e) / T is above its fp32 value for some and below for others; rows hold -inf."""
+    say(f"temperature {temperature} {rows} {vocab}")
+    x, index, top, w = inputs(rows, rows, vocab, 12, "f16", "f32", missing=False)
+    x[:, 700:740] = -float("inf")
+    index[:] = torch.arange(12, dtype=torch.int32) * 50
+    check(x, index, top, w, temperature)
 
 
 @pytest.mark.parametrize("rows", [0, 1, 2, 15, 16, 17, 255, 300, 1025])

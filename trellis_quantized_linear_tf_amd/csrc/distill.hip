@@ -402,7 +402,10 @@ size_t distill_workspace(int dtype, int rows, int vocab, int) {
 hipError_t launch_distill(const DistillArgs& args, hipStream_t stream) {
   DistillArgs a = args;
   const double c = 1.4426950408889634 / (double)a.temperature;
-  a.inv = 1.f / a.temperature, a.c = (float)c, a.c_low = (float)(c - (double)a.c);
+  a.inv = 1.f / a.temperature, a.c = (float)c;
+  // The low part is above 0, so that a difference of -inf meets no +inf and no 0 in it.
+  if ((double)a.c > c) a.c = nextafterf(a.c, 0.f);
+  a.c_low = fmaxf((float)(c - (double)a.c), 1.2e-38f);
   if (a.dtype == TF_DT_F32) launch<TF_DT_F32>(a, stream);
   if (a.dtype == TF_DT_F16) launch<TF_DT_F16>(a, stream);
   if (a.dtype == TF_DT_BF16) launch<TF_DT_BF16>(a, stream);
