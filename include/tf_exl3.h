@@ -288,8 +288,8 @@ int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int 
  * head's logits, and the distillation loss that trains a drafter on a teacher's
  * top logits. No page defines them; each formula is stated here.
  *
- * Strides are in elements. Innermost dimensions are contiguous (stride 1). What
- * lives on the device (lengths, page numbers, masks, node numbers, parents,
+ * Strides are in elements. Innermost dimensions are contiguous (stride 1); a stride
+ * over a dimension of 1 is not looked at. What lives on the device (lengths, page numbers, masks, node numbers, parents,
  * tokens) cannot be refused on the host: every kernel bounds it before an
  * address is made of it, as stated at each call. A workspace belongs to one call
  * at a time, needs no initial contents and may be used again, or freed in

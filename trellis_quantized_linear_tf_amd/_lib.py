@@ -259,8 +259,17 @@ def _same_gpu(*tensors) -> None:
             raise ValueError("all tensors must be on one GPU")
 
 
+_raw_stream = None
+
+
 def _stream(t) -> int:
-    return _torch().cuda.current_stream(t.get_device()).cuda_stream
+    """The current stream's handle on the tensor's GPU, by torch's short cut where it has one."""
+    global _raw_stream
+    if _raw_stream is None:
+        torch = _torch()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def rot_in(x, suh, z=None):

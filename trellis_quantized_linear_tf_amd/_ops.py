@@ -10,7 +10,7 @@ and what happens to out-of-range values on the device, stand in include/tf_exl3.
 
 from __future__ import annotations
 
-import ctypes
+import struct
 
 from . import _lib
 from ._lib import _check, _dt_code, _stream, _torch, load
@@ -70,11 +70,11 @@ def _floats():
     return (torch.float32, torch.float16, torch.bfloat16)
 
 
-_L3 = ctypes.c_int64 * 3
-
-
-def _strides(t):
-    return _L3(*(s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape)))  # a dimension of 1 has any stride
+# Every call looks its arguments over with one chain of comparisons, which implies all of
+# the checks below and costs a few microseconds; only a call that does not pass it goes
+# through them one by one, for the message (or because a dimension of 1 has an odd stride).
+_ATTENTION = struct.Struct("@9if10QN19q")
+_APPEND = struct.Struct("@8i8Q13q")
 
 
 def _check_cache(k_cache, v_cache, table, lengths, dtypes, batch, heads, dim):
@@ -87,16 +87,7 @@ def _check_cache(k_cache, v_cache, table, lengths, dtypes, batch, heads, dim):
     _need("lengths", lengths, 1, (torch.int32,), (batch,))
 
 
-def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, out=None):
-    """out[batch][nodes][q_heads][dim]: attention of drafted nodes over their sequence's cache
-    and, by a mask, over each other (tf_exl3_tree_attention).
-
-    q [batch][nodes][q_heads][dim], k and v [batch][nodes][kv_heads][dim] of fp16 or bf16: the
-    nodes' own rows (views of a fused projection's rows will do). mask int64 [batch][nodes]:
-    bit t of a node's mask says that it sees node t (1..64 nodes). k_cache, v_cache [pages]
-    [page_size][kv_heads][dim], in any order of memory with contiguous rows; table int32
-    [batch][table_pages]; lengths int32 [batch]: positions in the cache, all of them seen.
-    scale defaults to dim ** -0.5. A node that sees nothing gets zeros."""
+def _check_tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, out):
     torch = _torch()
     _need("q", q, 4, _halves())
     batch, nodes, hq, dim = q.shape
@@ -110,28 +101,64 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
     if out is not None:
         _need("out", out, 4, same, (batch, nodes, hq, dim))
     _one_gpu(q, k, v, mask, k_cache, v_cache, table, lengths, out)
+
+
+def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, out=None):
+    """out[batch][nodes][q_heads][dim]: attention of drafted nodes over their sequence's cache
+    and, by a mask, over each other (tf_exl3_tree_attention).
+
+    q [batch][nodes][q_heads][dim], k and v [batch][nodes][kv_heads][dim] of fp16 or bf16: the
+    nodes' own rows (views of a fused projection's rows will do). mask int64 [batch][nodes]:
+    bit t of a node's mask says that it sees node t (1..64 nodes). k_cache, v_cache [pages]
+    [page_size][kv_heads][dim], in any order of memory with contiguous rows; table int32
+    [batch][table_pages]; lengths int32 [batch]: positions in the cache, all of them seen.
+    scale defaults to dim ** -0.5. A node that sees nothing gets zeros."""
+    torch = _torch()
+    dev = -1
+    try:
+        batch, nodes, hq, dim = shape = q.shape
+        rows, pages = k.shape, k_cache.shape
+        hkv, columns, t = rows[2], table.shape[1], q.dtype
+        sq, sk, sv, skc, svc = q.stride(), k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+        if (
+            (t is torch.bfloat16 or t is torch.float16)
+            and k.dtype is t and v.dtype is t and k_cache.dtype is t and v_cache.dtype is t
+            and rows == (batch, nodes, hkv, dim) and v.shape == rows
+            and len(pages) == 4 and pages[2] == hkv and pages[3] == dim and pages[0] > 0 and pages[1] > 0
+            and v_cache.shape == pages
+            and mask.dtype is torch.int64 and mask.shape == (batch, nodes) and mask.is_contiguous()
+            and table.dtype is torch.int32 and table.shape == (batch, columns) and table.stride(1) == 1
+            and lengths.dtype is torch.int32 and lengths.shape == (batch,) and lengths.stride(0) == 1
+            and sq[3] == sk[3] == sv[3] == skc[3] == svc[3] == 1
+            and (out is None or out.dtype is t and out.shape == shape and out.stride(3) == 1)
+        ):
+            d = q.get_device()
+            if (
+                d == k.get_device() == v.get_device() == mask.get_device() == k_cache.get_device()
+                == v_cache.get_device() == table.get_device() == lengths.get_device()
+                and (out is None or out.get_device() == d)
+            ):
+                dev = d
+    except (AttributeError, IndexError, RuntimeError, ValueError):
+        pass
+    if dev < 0:
+        _check_tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, out)
     if out is None:
-        out = torch.empty((batch, nodes, hq, dim), dtype=q.dtype, device=q.device)
-    a = _lib.TreeAttentionArgs(
-        _dt_code(q.dtype), batch, nodes, hq, hkv, dim, k_cache.shape[0], k_cache.shape[1], table.shape[1],
-        dim ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), out.data_ptr())
-    a.q_stride, a.k_stride, a.v_stride = _strides(q), _strides(k), _strides(v)
-    a.k_cache_stride, a.v_cache_stride, a.out_stride = _strides(k_cache), _strides(v_cache), _strides(out)
-    a.table_stride = table.stride(0)
+        out = q.new_empty(shape)
     lib = load()
-    a.workspace_bytes = lib.tf_exl3_tree_attention_workspace(a)
-    ws = _workspace(a.workspace_bytes, q)
-    a.workspace = ws.data_ptr()
+    a = _lib.TreeAttentionArgs(_dt_code(t), batch, nodes, hq, hkv, dim, pages[0], pages[1], columns)
+    need = lib.tf_exl3_tree_attention_workspace(a)
+    ws = _workspace(need, q)
+    _ATTENTION.pack_into(
+        a, 0, a.dtype, batch, nodes, hq, hkv, dim, pages[0], pages[1], columns, dim ** -0.5 if scale is None else scale,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), need, *sq[:3], *sk[:3], *sv[:3],
+        *skc[:3], *svc[:3], *out.stride()[:3], table.stride(0))
     _check(lib.tf_exl3_tree_attention(a, _stream(q)))
     return out
 
 
-def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None):
-    """Writes rows of k and v [batch][tokens][kv_heads][dim] behind the lengths[b] positions
-    that a sequence has in the cache (tf_exl3_cache_append). nodes int32 [batch][tokens] and
-    counts int32 [batch] choose them: position lengths[b] + j takes row nodes[b][j], for
-    j < counts[b] (verify_tree's `accepted` and `count` fit). lengths stays as it is."""
+def _check_cache_append(k, v, k_cache, v_cache, table, lengths, nodes, counts):
     torch = _torch()
     dtypes = (torch.float16, torch.bfloat16, torch.float32, torch.int8, torch.uint8, torch.int16, torch.float8_e4m3fn,
               torch.float8_e5m2)
@@ -146,10 +173,46 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None
     if counts is not None:
         _need("counts", counts, 1, (torch.int32,), (batch,))
     _one_gpu(k, v, k_cache, v_cache, table, lengths, nodes, counts)
-    a = _lib.CacheAppendArgs(
-        k.element_size(), batch, tokens, heads, dim, k_cache.shape[0], k_cache.shape[1], table.shape[1],
-        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-        _ptr(nodes), _ptr(counts), _strides(k), _strides(v), _strides(k_cache), _strides(v_cache), table.stride(0))
+
+
+def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None):
+    """Writes rows of k and v [batch][tokens][kv_heads][dim] behind the lengths[b] positions
+    that a sequence has in the cache (tf_exl3_cache_append). nodes int32 [batch][tokens] and
+    counts int32 [batch] choose them: position lengths[b] + j takes row nodes[b][j], for
+    j < counts[b] (verify_tree's `accepted` and `count` fit). lengths stays as it is."""
+    torch = _torch()
+    dev = -1
+    try:
+        batch, tokens, heads, dim = rows = k.shape
+        pages, columns, t = k_cache.shape, table.shape[1], k.dtype
+        sk, sv, skc, svc = k.stride(), v.stride(), k_cache.stride(), v_cache.stride()
+        if (
+            (t is torch.bfloat16 or t is torch.float16)
+            and v.dtype is t and k_cache.dtype is t and v_cache.dtype is t and v.shape == rows
+            and len(pages) == 4 and pages[2] == heads and pages[3] == dim and pages[0] > 0 and pages[1] > 0
+            and v_cache.shape == pages
+            and table.dtype is torch.int32 and table.shape == (batch, columns) and table.stride(1) == 1
+            and lengths.dtype is torch.int32 and lengths.shape == (batch,) and lengths.stride(0) == 1
+            and sk[3] == sv[3] == skc[3] == svc[3] == 1
+            and (nodes is None or nodes.dtype is torch.int32 and nodes.shape == (batch, tokens) and nodes.is_contiguous())
+            and (counts is None or counts.dtype is torch.int32 and counts.shape == (batch,) and counts.stride(0) == 1)
+        ):
+            d = k.get_device()
+            if (
+                d == v.get_device() == k_cache.get_device() == v_cache.get_device() == table.get_device()
+                == lengths.get_device()
+                and (nodes is None or nodes.get_device() == d) and (counts is None or counts.get_device() == d)
+            ):
+                dev = d
+    except (AttributeError, IndexError, RuntimeError, ValueError):
+        pass
+    if dev < 0:
+        _check_cache_append(k, v, k_cache, v_cache, table, lengths, nodes, counts)
+    a = _lib.CacheAppendArgs()
+    _APPEND.pack_into(
+        a, 0, k.element_size(), batch, tokens, heads, dim, pages[0], pages[1], columns, k.data_ptr(), v.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), _ptr(nodes) or 0, _ptr(counts) or 0,
+        *sk[:3], *sv[:3], *skc[:3], *svc[:3], table.stride(0))
     _check(load().tf_exl3_cache_append(a, _stream(k)))
 
 
@@ -166,6 +229,20 @@ def _check_drafts(logits, tokens, u, temperature):
     return batch, nodes, vocab
 
 
+def _drafts_fit(torch, logits, tokens, u, temperature):
+    """Whether the arguments that both verifications have pass their checks, and (batch, nodes, vocab)."""
+    sizes = batch, nodes, vocab = logits.shape
+    t, d, pairs = logits.dtype, logits.get_device(), (batch, nodes)
+    return (
+        (t is torch.float32 or t is torch.bfloat16 or t is torch.float16) and logits.stride(2) == 1
+        and tokens.dtype is torch.int32 and tokens.shape == pairs and tokens.is_contiguous()
+        and u.dtype is torch.float32 and u.shape == pairs and u.is_contiguous()
+        and d == tokens.get_device() == u.get_device() and d >= 0
+        and (temperature is None or temperature.dtype is torch.float32 and temperature.shape == (batch,)
+             and temperature.stride(0) == 1 and temperature.get_device() == d)
+    ), sizes
+
+
 def verify_tree(logits, tokens, parents, u, temperature=None):
     """(accepted int32 [batch][nodes], count int32 [batch], next int32 [batch]): the path of a
     drafted tree that the target's own samples follow (tf_exl3_verify_tree).
@@ -176,12 +253,20 @@ def verify_tree(logits, tokens, parents, u, temperature=None):
     largest logit, None for 1. accepted holds the path's nodes, then -1; next the token
     sampled at its end."""
     torch = _torch()
-    batch, nodes, vocab = _check_drafts(logits, tokens, u, temperature)
-    _need("parents", parents, 2, (torch.int32,), (batch, nodes))
-    _whole("parents", parents)
-    _one_gpu(logits, tokens, parents, u, temperature)
-    accepted = torch.empty((batch, nodes), dtype=torch.int32, device=logits.device)
-    count, after = torch.empty((2, batch), dtype=torch.int32, device=logits.device)
+    fit = False
+    try:
+        fit, (batch, nodes, vocab) = _drafts_fit(torch, logits, tokens, u, temperature)
+        fit = fit and (parents.dtype is torch.int32 and parents.shape == (batch, nodes) and parents.is_contiguous()
+                       and parents.get_device() == logits.get_device())
+    except (AttributeError, IndexError, RuntimeError, ValueError):
+        pass
+    if not fit:
+        batch, nodes, vocab = _check_drafts(logits, tokens, u, temperature)
+        _need("parents", parents, 2, (torch.int32,), (batch, nodes))
+        _whole("parents", parents)
+        _one_gpu(logits, tokens, parents, u, temperature)
+    accepted = tokens.new_empty((batch, nodes))
+    count, after = tokens.new_empty((batch,)), tokens.new_empty((batch,))
     lib = load()
     need = lib.tf_exl3_verify_workspace(batch, nodes, vocab)
     ws = _workspace(need, logits)
@@ -202,10 +287,18 @@ def verify_chain(logits, tokens, q, u, temperature=None):
     the last for the token after them. count is 1 + the accepted drafts; next comes from
     max(p - q, 0) where a draft was refused, from p where all were accepted."""
     torch = _torch()
-    batch, nodes, vocab = _check_drafts(logits, tokens, u, temperature)
-    _need("q", q, 3, (torch.float32,), (batch, max(nodes - 1, 0), vocab))
-    _one_gpu(logits, tokens, q, u, temperature)
-    count, after = torch.empty((2, batch), dtype=torch.int32, device=logits.device)
+    fit = False
+    try:
+        fit, (batch, nodes, vocab) = _drafts_fit(torch, logits, tokens, u, temperature)
+        fit = fit and (q.dtype is torch.float32 and q.shape == (batch, nodes - 1, vocab) and q.stride(2) == 1
+                       and q.get_device() == logits.get_device())
+    except (AttributeError, IndexError, RuntimeError, ValueError):
+        pass
+    if not fit:
+        batch, nodes, vocab = _check_drafts(logits, tokens, u, temperature)
+        _need("q", q, 3, (torch.float32,), (batch, max(nodes - 1, 0), vocab))
+        _one_gpu(logits, tokens, q, u, temperature)
+    count, after = tokens.new_empty((batch,)), tokens.new_empty((batch,))
     lib = load()
     need = lib.tf_exl3_verify_workspace(batch, nodes, vocab)
     ws = _workspace(need, logits)
@@ -218,18 +311,33 @@ def verify_chain(logits, tokens, q, u, temperature=None):
 
 def _distill(logits, index, top, weight, temperature, want_loss, want_grad):
     torch = _torch()
-    _need("logits", logits, 2, _floats())
-    rows, vocab = logits.shape
-    _need("index", index, 2, (torch.int32,), (rows, None))
-    _need("top", top, 2, _floats(), tuple(index.shape))
-    _whole("index", index)
-    _whole("top", top)
-    if want_grad:
-        _need("weight", weight, 1, (torch.float32,), (rows,))
-        _whole("weight", weight)
-    _one_gpu(logits, index, top, weight)
+    fit = False
+    try:
+        rows, vocab = logits.shape
+        t, y, d, entries = logits.dtype, top.dtype, logits.get_device(), index.shape
+        fit = (
+            (t is torch.float32 or t is torch.bfloat16 or t is torch.float16) and logits.stride(1) == 1
+            and (y is t or y is torch.float32 or y is torch.bfloat16 or y is torch.float16)
+            and index.dtype is torch.int32 and len(entries) == 2 and entries[0] == rows and index.is_contiguous()
+            and top.shape == entries and top.is_contiguous() and d == index.get_device() == top.get_device() and d >= 0
+            and (weight is None and not want_grad or weight.dtype is torch.float32 and weight.shape == (rows,)
+                 and weight.is_contiguous() and weight.get_device() == d)
+        )
+    except (AttributeError, IndexError, RuntimeError, ValueError):
+        pass
+    if not fit:
+        _need("logits", logits, 2, _floats())
+        rows, vocab = logits.shape
+        _need("index", index, 2, (torch.int32,), (rows, None))
+        _need("top", top, 2, _floats(), tuple(index.shape))
+        _whole("index", index)
+        _whole("top", top)
+        if want_grad:
+            _need("weight", weight, 1, (torch.float32,), (rows,))
+            _whole("weight", weight)
+        _one_gpu(logits, index, top, weight)
     loss = torch.empty((rows,), dtype=torch.float32, device=logits.device) if want_loss else None
-    grad = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device) if want_grad else None
+    grad = logits.new_empty((rows, vocab)) if want_grad else None
     lib = load()
     code = _dt_code(logits.dtype)
     need = lib.tf_exl3_distill_workspace(code, rows, vocab, index.shape[1])

@@ -32,6 +32,13 @@ size_t extent(int64_t n0, int64_t n1, int64_t n2, int64_t d, const int64_t* s, s
   return (size_t)((n0 - 1) * s[0] + (n1 - 1) * s[1] + (n2 - 1) * s[2] + d) * elem;
 }
 
+// A stride over a dimension of 1 is never used, whatever it is.
+void settle(int64_t n0, int64_t n1, int64_t n2, int64_t* s) {
+  if (n0 <= 1) s[0] = 0;
+  if (n1 <= 1) s[1] = 0;
+  if (n2 <= 1) s[2] = 0;
+}
+
 bool strides_ok(const int64_t* s, int64_t multiple) {
   for (int i = 0; i < 3; ++i)
     if (s[i] < 0 || s[i] > kMaxStride || s[i] % multiple != 0) return false;
@@ -76,8 +83,16 @@ size_t tf_exl3_tree_attention_workspace(const tf_exl3_tree_attention_args* a) {
   return tf_exl3::tree_attention_workspace(*a);
 }
 
-int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* a, void* stream) {
-  if (a == nullptr) return TF_E_NULL;
+int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* args, void* stream) {
+  if (args == nullptr) return TF_E_NULL;
+  tf_exl3_tree_attention_args settled = *args;
+  tf_exl3_tree_attention_args* a = &settled;
+  settle(a->batch, a->nodes, a->q_heads, a->q_stride);
+  settle(a->batch, a->nodes, a->kv_heads, a->k_stride);
+  settle(a->batch, a->nodes, a->kv_heads, a->v_stride);
+  settle(a->pages, a->page_size, a->kv_heads, a->k_cache_stride);
+  settle(a->pages, a->page_size, a->kv_heads, a->v_cache_stride);
+  settle(a->batch, a->nodes, a->q_heads, a->out_stride);
   int st = attention_sizes(a);
   if (st == TF_OK) st = cache_sizes(a->pages, a->page_size, a->table_pages, a->table_stride);
   if (st != TF_OK) return st;
@@ -118,8 +133,14 @@ int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* a, void* stream) {
   return e == hipSuccess ? TF_OK : TF_E_LAUNCH;
 }
 
-int tf_exl3_cache_append(const tf_exl3_cache_append_args* a, void* stream) {
-  if (a == nullptr) return TF_E_NULL;
+int tf_exl3_cache_append(const tf_exl3_cache_append_args* args, void* stream) {
+  if (args == nullptr) return TF_E_NULL;
+  tf_exl3_cache_append_args settled = *args;
+  tf_exl3_cache_append_args* a = &settled;
+  settle(a->batch, a->tokens, a->kv_heads, a->k_stride);
+  settle(a->batch, a->tokens, a->kv_heads, a->v_stride);
+  settle(a->pages, a->page_size, a->kv_heads, a->k_cache_stride);
+  settle(a->pages, a->page_size, a->kv_heads, a->v_cache_stride);
   if (a->elem_bytes != 1 && a->elem_bytes != 2 && a->elem_bytes != 4) return TF_E_DTYPE;
   if (a->batch < 0 || a->batch > kMaxBatch || a->tokens < 0 || a->tokens > (1 << 30) || a->kv_heads < 1 ||
       a->head_dim < 1 || (int64_t)a->kv_heads * a->head_dim > (1 << 24))
