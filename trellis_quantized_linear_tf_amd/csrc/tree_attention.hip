@@ -38,7 +38,7 @@ struct AttnPlan {
   int units;            // runs, at most
   int target;           // runs to aim for over all sequences; 0: one each
   int min_tiles;        // of a run
-  float c;              // |scale| log2(e)
+  float c, slack;       // |scale| log2(e); 8 / c
   bool negate;          // scale < 0
   FastDiv by_group, by_page, by_row_tiles, by_heads, by_quads;
   int2* seq;            // [batch] first run, runs
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
   // The loader's part: chunk `chunk` of rows tid / NC, + kStep, ...
   const int chunk = tid % NC, lrow = tid / NC;
   x = arguments();
-  const float scale_c = x->p.c;
+  const float scale_c = x->p.c, slack = x->p.slack;
   const bool have = chunk * 8 < x->a.head_dim;
   const T* kc = static_cast<const T*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * 8;
   const T* vc = static_cast<const T*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * 8;
@@ -359,6 +359,8 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
       }
     }
 
+    // The base m of a row's exponents is raised, and its sums scaled, only where a score has
+    // grown past it by a factor of 2^8: probabilities up to that lose nothing in any type here.
     float top[RT];
     bool grow = false;
 #pragma unroll
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) v = fmaxf(v, s[t][rt][i]);
       top[rt] = fmaxf(m[rt], groups_max(v));
-      grow = grow || top[rt] > m[rt];
+      grow = grow || top[rt] > m[rt] + slack;
     }
     if (__ballot(grow)) {
 #pragma unroll
@@ -627,6 +629,7 @@ hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream
   // A scale of 0 keeps masked scores apart from others: the smallest factor does the same to sums.
   const float c = fabsf(a.scale) * 1.4426950408889634f;
   l.p.c = c > 1.2e-38f ? c : 1.2e-38f;
+  l.p.slack = fminf(8.f / l.p.c, 3e38f);
   l.p.negate = a.scale < 0.f;
   l.p.by_group = fast_div(l.p.group), l.p.by_page = fast_div(a.page_size);
   l.p.by_row_tiles = fast_div(l.p.row_tiles), l.p.by_heads = fast_div(a.kv_heads);
