@@ -15,9 +15,11 @@
 // in fp32; probabilities are rounded to the inputs' type for the second product (half a
 // unit in the last place each, which the sum of fp32 probabilities does not see).
 //
-// Positions are split over workgroups so that the chip is full whatever the lengths are:
-// every workgroup finds its run from the lengths on the device. Runs leave fp32 outputs
-// with their maximum and sum, and a second kernel joins them.
+// All tiles of all sequences, heads and row tiles stand in one line, which the workgroups,
+// as many as the chip holds at a time, cut into equal pieces, whatever the lengths are:
+// every workgroup finds its piece from the lengths on the device. Where a piece ends within a
+// sequence's tiles, it leaves fp32 outputs with their base and sum, and a second kernel
+// joins them.
 #include <math.h>
 
 #include "ops_device.hpp"
@@ -32,18 +34,26 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// Where a sequence's tiles begin in the line of all of them, and how many one row tile has.
+struct SeqTiles {
+  int64_t begin;
+  int tiles, piece;  // piece: tiles of a workgroup
+};
+
 struct AttnPlan {
-  int rows, group;      // of one kv head: nodes * group
-  int row_tiles;        // workgroups that share a run's positions
-  int units;            // runs, at most
-  int target;           // runs to aim for over all sequences; 0: one each
-  int min_tiles;        // of a run
-  float c, slack;       // |scale| log2(e); 8 / c
-  bool negate;          // scale < 0
-  FastDiv by_group, by_page, by_row_tiles, by_heads, by_quads;
-  int2* seq;            // [batch] first run, runs
-  float2* stat;         // [unit][head][row] maximum (in log2 units), sum
-  float* part;          // [unit][head][row][dim]
+  int rows, group;     // of one kv head: nodes * group
+  int row_tiles;       // of one kv head
+  int groups;          // kv_heads * row_tiles, each with all tiles of a sequence
+  int workgroups;      // pieces, at most; 0: one for each group of each sequence
+  int min_piece;       // tiles
+  float c, slack;      // |scale| log2(e); 8 / c
+  bool negate;         // scale < 0
+  uint32_t page_bytes, slot_bytes;  // of both caches, where they are the same and below 4 GiB
+  int step_cols, step_slots;        // a tile in pages and slots
+  FastDiv by_group, by_page, by_row_tiles, by_rows, by_groups;
+  SeqTiles* seq;       // [batch]
+  float2* stat;        // [2 pieces][rows of a tile] base (in log2 units), sum
+  float* part;         // [2 pieces][rows of a tile][dim]
 };
 
 // The kernel's arguments, read from the argument segment where they are needed: the
@@ -103,52 +113,69 @@ __device__ __forceinline__ int cached(ArgPtr x, int b) {
   return (int)(len < 0 ? 0 : len > room ? room : len);
 }
 
-struct Run {
-  int b, first, runs;  // sequence, its first run, its runs
-  int begin, end;      // in tiles
+// n / d, of values that seldom need 64 bits.
+__device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {
+  if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
+  return n / d;
+}
+
+// A value that all lanes have, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
+// A stretch of one group's tiles.
+struct Segment {
+  int b, group, tile, left;  // left: tiles of the piece from here on
+  int64_t begin;             // of the sequence in the line
+  int piece;
 };
 
-// Run `unit` of the batch: a sequence of t tiles is cut into ceil(t / P) runs of equal size,
-// P = max(min_tiles, ceil(all tiles / target)), so there are at most target + batch.
 template <int KT>
-__device__ __forceinline__ bool find_run(ArgPtr x, int unit, Run* r) {
-  const int batch = x->a.batch, nodes = x->a.nodes, target = x->p.target;
-  if (target == 0) {
-    r->b = unit, r->first = unit, r->runs = 1, r->begin = 0;
-    r->end = (cached(x, unit) + nodes + KT - 1) / KT;
+__device__ __forceinline__ int tiles_of(ArgPtr x, int b) { return (cached(x, b) + x->a.nodes + KT - 1) / KT; }
+
+// Where the workgroup's piece begins.
+template <int KT>
+__device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
+  const int batch = x->a.batch, groups = x->p.groups, workgroups = x->p.workgroups;
+  if (workgroups == 0) {
+    s->b = copy(&x->p.by_groups).div(w), s->group = w - s->b * groups;
+    s->tile = 0, s->left = uniform(tiles_of<KT>(x, s->b)), s->begin = 0, s->piece = 0;
     return true;
   }
   const int lane = threadIdx.x & 63;
   int64_t all = 0;
-  for (int b = lane; b < batch; b += 64) all += (cached(x, b) + nodes + KT - 1) / KT;
+  for (int b = lane; b < batch; b += 64) all += tiles_of<KT>(x, b);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
-  const int64_t aim = (all + target - 1) / target;
-  const int size = (int)(aim < x->p.min_tiles ? x->p.min_tiles : aim);
-  int base = 0;
-  for (int b0 = 0; b0 < batch; b0 += 64) {
-    const int tiles = b0 + lane < batch ? (cached(x, b0 + lane) + nodes + KT - 1) / KT : 0;
-    const int runs = (tiles + size - 1) / size;
-    int incl = runs;
+  all = uniform(all) * groups;
+  const int64_t even = divide(all + workgroups - 1, workgroups);
+  s->piece = uniform((int)(even < x->p.min_piece ? x->p.min_piece : even));
+  const int64_t from = (int64_t)w * s->piece;
+  if (from >= all) return false;
+  s->left = (int)(all - from < s->piece ? all - from : s->piece);
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += 64) {
+    const int tiles = b0 + lane < batch ? tiles_of<KT>(x, b0 + lane) : 0;
+    int64_t end = (int64_t)tiles * groups;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(incl, o);
-      if (lane >= o) incl += up;
+      const int64_t up = __shfl_up(end, o);
+      if (lane >= o) end += up;
     }
-    const uint64_t hit = __ballot(base + incl > unit);
+    end += base;
+    const uint64_t hit = __ballot(end > from);
     if (hit) {
-      const int at = __builtin_ctzll(hit);
-      r->b = b0 + at;
-      r->runs = __builtin_amdgcn_readlane(runs, at);
-      r->first = base + __builtin_amdgcn_readlane(incl, at) - r->runs;
-      const int t = __builtin_amdgcn_readlane(tiles, at), each = (t + r->runs - 1) / r->runs;
-      r->begin = min(t, (unit - r->first) * each);
-      r->end = min(t, r->begin + each);
+      const int at = __builtin_ctzll(hit), n = __builtin_amdgcn_readlane(tiles, at);
+      s->b = b0 + at;
+      s->begin = uniform(__shfl(end, at)) - (int64_t)n * groups;
+      s->group = uniform((int)divide(from - s->begin, n));
+      s->tile = (int)(from - s->begin - (int64_t)s->group * n);
       return true;
     }
-    base += __builtin_amdgcn_readlane(incl, 63);
+    base = uniform(__shfl(end, 63));
   }
-  return false;
 }
 
 // Shared memory holds rows of DP elements in 16-byte chunks; chunk c of row r stands at
@@ -181,8 +208,9 @@ __device__ __forceinline__ uint32_t seen_of(uint64_t seen, int node, int left) {
   return tree & (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1);
 }
 
-template <int DT, int DP, int RT, int RG, int KG, int KW>
-__global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) {
+// S: tiles whose keys and values are on their way to registers.
+template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int WAVES>
+__global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(AttnArgs) {
   typedef uint16_t T;
   constexpr int kThreads = RG * KG * 64, KT = KG * KW, NC = DP / 8, NK = KW / 16, NB = KW / 32, ND = DP / 16, NQ = DP / 32;
   constexpr int kStep = kThreads / NC, kLoads = KT / kStep;  // rows between a thread's loads, and how many
@@ -193,21 +221,24 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
   __shared__ float2 join_stat[KG > 1 ? (KG - 1) * RG * 64 : 1];
   __shared__ int odd_values;
 
-  // Row tiles of one run go to one XCD (workgroups go round the eight of them), whose L2
-  // then serves the run's keys and values to all but the first.
   ArgPtr x = arguments();
-  const int kv_heads = x->a.kv_heads, nodes = x->a.nodes;
-  const int k = blockIdx.x >> 3, up = copy(&x->p.by_row_tiles).div(k);
-  const int row_tile = k - up * x->p.row_tiles, uh = up * 8 + (blockIdx.x & 7);
-  const int unit = copy(&x->p.by_heads).div(uh), g = uh - unit * kv_heads;
-  if (unit >= x->p.units) return;
-  Run run;
-  if (!find_run<KT>(x, unit, &run)) return;
-  const int b = run.b, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int rg = wave % RG, kg = wave / RG, lg = lane >> 4;
-  if (x->p.target && unit == run.first && g == 0 && row_tile == 0 && tid == 0) x->p.seq[b] = make_int2(run.first, run.runs);
-  const int len = cached(x, b);
-  const int stop = min(run.end * KT, len + nodes);  // positions of the run: begin * KT .. stop - 1
+  Segment seg;
+  if (!find_piece<KT>(x, blockIdx.x, &seg)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rg = wave % RG, kg = wave / RG;
+  bool first = true;
+  for (;;) {
+  x = arguments();
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // what depends on it is worked out again and not kept over segments
+  const int lane = tid & 63, lg = lane >> 4;
+  const int nodes = x->a.nodes, b = seg.b;
+  const int g = copy(&x->p.by_row_tiles).div(seg.group), row_tile = seg.group - g * x->p.row_tiles;
+  const int len = uniform(cached(x, b)), tiles = (len + nodes + KT - 1) / KT;
+  const int begin = seg.tile * KT, until = min(tiles, seg.tile + seg.left);
+  const int stop = min(until * KT, len + nodes);  // positions of the segment: begin .. stop - 1
+  const bool whole = seg.tile == 0 && until == tiles;
+  if (x->p.workgroups && seg.group == 0 && seg.tile == 0 && tid == 0) x->p.seq[b] = {seg.begin, tiles, seg.piece};
   if (tid == 0) odd_values = 0;
 
   // The rows' queries and masks.
@@ -242,34 +273,57 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
   const bool have = chunk * 8 < x->a.head_dim;
   const T* kc = static_cast<const T*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * 8;
   const T* vc = static_cast<const T*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * 8;
-  const int64_t kc_page = x->a.k_cache_stride[0], kc_slot = x->a.k_cache_stride[1];
-  const int64_t vc_page = x->a.v_cache_stride[0], vc_slot = x->a.v_cache_stride[1];
+  const uint32_t page_bytes = x->p.page_bytes, slot_bytes = x->p.slot_bytes;  // page_bytes 0: wide or different strides
   const int32_t* table = x->a.table + b * x->a.table_stride;
   const int pages = x->a.pages, page_size = x->a.page_size;
+  const int step_cols = x->p.step_cols, step_slots = x->p.step_slots;
+  u32x4 kr[S][kLoads], vr[S][kLoads];
+  // A row's page and slot go on by a tile at a time; rows behind the cache's end look at its
+  // last page, which is there, and are not used.
+  int page[kLoads] = {}, col[kLoads], slot[kLoads];
   const FastDiv by_page = copy(&x->p.by_page);
-  u32x4 kr[kLoads], vr[kLoads];
-  int page[kLoads] = {};
-  // Columns of the table for the tile at `at`; the nodes' rows look the last one up.
-  auto look_up = [&](int at) {
+  const int last_col = len > 0 ? by_page.div(len - 1) : 0;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int j = begin + lrow + i * kStep;
+    col[i] = by_page.div(j);
+    slot[i] = j - col[i] * page_size;
+  }
+  auto look_up = [&]() {
     if (len > 0) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) page[i] = table[by_page.div(min(at + lrow + i * kStep, len - 1))];
+      for (int i = 0; i < kLoads; ++i) page[i] = *reinterpret_cast<const int32_t*>(
+          reinterpret_cast<const char*>(table) + (uint32_t)min(col[i], last_col) * 4u);
     }
   };
-  // A tile's rows; behind the run's end the last row again, which is not used.
-  auto load = [&](int at) {
+  auto advance = [&]() {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      slot[i] += step_slots, col[i] += step_cols;
+      const bool wrap = slot[i] >= page_size;
+      slot[i] -= wrap ? page_size : 0, col[i] += wrap;
+    }
+  };
+  auto load = [&](int at, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads]) {
     const bool edge = at + KT > min(len, stop);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int j = edge ? min(at + lrow + i * kStep, stop - 1) : at + lrow + i * kStep;
-      const int64_t pg = (uint32_t)page[i] < (uint32_t)pages ? page[i] : 0;
-      const int64_t slot = j - by_page.div(j) * page_size;
-      const T* kp = kc + pg * kc_page + slot * kc_slot;
-      const T* vp = vc + pg * vc_page + slot * vc_slot;
+      const uint32_t pg = (uint32_t)page[i] < (uint32_t)pages ? page[i] : 0;
+      const T *kp, *vp;
+      if (page_bytes) {
+        const uint64_t off = (uint64_t)pg * page_bytes + (uint64_t)(uint32_t)slot[i] * slot_bytes;
+        kp = reinterpret_cast<const T*>(reinterpret_cast<const char*>(kc) + off);
+        vp = reinterpret_cast<const T*>(reinterpret_cast<const char*>(vc) + off);
+      } else {
+        const ArgPtr y = arguments();
+        kp = kc + pg * y->a.k_cache_stride[0] + slot[i] * y->a.k_cache_stride[1];
+        vp = vc + pg * y->a.v_cache_stride[0] + slot[i] * y->a.v_cache_stride[1];
+      }
       if (edge) {
         const ArgPtr y = arguments();
-        const T* kt = static_cast<const T*>(y->a.k) + b * y->a.k_stride[0] + g * y->a.k_stride[2] + (j - len) * y->a.k_stride[1] + chunk * 8;
-        const T* vt = static_cast<const T*>(y->a.v) + b * y->a.v_stride[0] + g * y->a.v_stride[2] + (j - len) * y->a.v_stride[1] + chunk * 8;
+        const int j = at + lrow + i * kStep, node = min(j, stop - 1) - len;  // behind the run's end its last row again
+        const T* kt = static_cast<const T*>(y->a.k) + b * y->a.k_stride[0] + g * y->a.k_stride[2] + node * y->a.k_stride[1] + chunk * 8;
+        const T* vt = static_cast<const T*>(y->a.v) + b * y->a.v_stride[0] + g * y->a.v_stride[2] + node * y->a.v_stride[1] + chunk * 8;
         kp = j < len ? kp : kt;
         vp = j < len ? vp : vt;
       }
@@ -290,11 +344,14 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
   const int vrow = lg * 4 + ((lane & 15) >> 2);  // of the 32 positions of a step, and 16 behind
   const u32x4* value_row = lds + kTile + (kg * KW + vrow) * NC;
 
-  int at = run.begin * KT;
   if (have) {
-    look_up(at);
-    load(at);
-    look_up(at + KT);
+    look_up();
+#pragma unroll
+    for (int st = 0; st < S; ++st) {
+      if (begin + st * KT < stop) load(begin + st * KT, kr[st], vr[st]);
+      advance();
+      look_up();
+    }
   } else {
     // Columns behind the head's are zero throughout.
 #pragma unroll
@@ -304,7 +361,11 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
       lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = u32x4(0u);
     }
   }
-  for (; at < stop; at += KT) {
+  for (int at0 = begin; at0 < stop; at0 += S * KT) {
+#pragma unroll
+  for (int st = 0; st < S; ++st) {
+    const int at = at0 + st * KT;
+    if (at >= stop) break;
     const bool edge = at + KT > min(len, stop);
     __syncthreads();  // the last tile has been used
     if (have) {
@@ -314,19 +375,20 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int j = at + lrow + i * kStep;
-          if (j >= stop) vr[i] = u32x4(0u);
-          if (j >= len && drop_nonfinite<DT>(vr[i])) odd_values = 1;
+          if (j >= stop) vr[st][i] = u32x4(0u);
+          if (j >= len && drop_nonfinite<DT>(vr[st][i])) odd_values = 1;
         }
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = lrow + i * kStep;
-        lds[r * NC + key_chunk<DP>(r, chunk)] = kr[i];
-        lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = vr[i];
+        lds[r * NC + key_chunk<DP>(r, chunk)] = kr[st][i];
+        lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = vr[st][i];
       }
-      if (at + KT < stop) {
-        load(at + KT);
-        look_up(at + 2 * KT);
+      if (at + S * KT < stop) {
+        load(at + S * KT, kr[st], vr[st]);
+        advance();
+        look_up();
       }
     }
     __syncthreads();
@@ -416,6 +478,7 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
         for (int rt = 0; rt < RT; ++rt) o[dt][rt] = mfma<DT>(vf, pf[kb][rt], o[dt][rt]);
       }
   }
+  }
 
   __syncthreads();
 #pragma unroll
@@ -448,14 +511,12 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
         }
       }
     }
-    if (kg > 0) return;
   }
-  if (!active) return;
-
+  if (kg == 0 && active) {
   x = arguments();
   const int dim = x->a.head_dim;
   if (odd_values) {
-    for (int j = max(len, run.begin * KT); j < stop; ++j) {
+    for (int j = max(len, begin); j < stop; ++j) {
       const T* row = static_cast<const T*>(x->a.v) + b * x->a.v_stride[0] + g * x->a.v_stride[2] + (j - len) * x->a.v_stride[1];
 #pragma unroll
       for (int dt = 0; dt < ND; ++dt) {
@@ -476,7 +537,7 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
   for (int rt = 0; rt < RT; ++rt) {
     const int r = row0 + rt * 16 + (lane & 15);
     if (r >= rows) continue;
-    if (run.runs == 1) {
+    if (whole) {
       const int node = by_group.div(r), head = g * group + r - node * group;
       T* out = static_cast<T*>(x->a.out) + b * x->a.out_stride[0] + node * x->a.out_stride[1] + head * x->a.out_stride[2] + lg * 4;
       const float inv = z[rt] == 0.f ? 0.f : 1.f / z[rt];
@@ -487,7 +548,7 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
           *reinterpret_cast<u32x2*>(out + dt * 16) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
         }
     } else {
-      const int64_t row = ((int64_t)unit * kv_heads + g) * rows + r;
+      const int64_t row = ((int64_t)blockIdx.x * 2 + !first) * (16 * RT * RG) + r - row_tile * (16 * RT * RG);
       if (lg == 0) x->p.stat[row] = make_float2(m[rt] == -INFINITY ? -INFINITY : m[rt] * scale_c, z[rt]);
       float* part = x->p.part + row * dim + lg * 4;
 #pragma unroll
@@ -495,33 +556,69 @@ __global__ __launch_bounds__(RG * KG * 64) void tree_attention_kernel(AttnArgs) 
         if (dt * 16 < dim) *reinterpret_cast<f32x4*>(part + dt * 16) = o[dt][rt];
     }
   }
+  }
+
+  seg.left -= until - seg.tile;
+  if (seg.left <= 0) return;
+  seg.tile = 0, first = false;
+  if (++seg.group == arguments()->p.groups) {
+    seg.begin += (int64_t)tiles * seg.group;
+    seg.group = 0, ++seg.b;
+  }
+  __syncthreads();
+  }
 }
 
-// Four columns of one row a thread: its runs, joined in order.
-template <int DT>
-__global__ __launch_bounds__(256) void tree_attention_join_kernel(tf_exl3_tree_attention_args a, AttnPlan p) {
-  const int b = blockIdx.y, f = blockIdx.x * 256 + threadIdx.x;
-  const int row = p.by_quads.div(f), d = (f - row * (a.head_dim / 4)) * 4;  // row: (head, row of the head)
+// One wave per row: the weights of the pieces that its tiles lie in, a lane each, then their
+// outputs, four columns a lane and as many pieces at a time as the wave has lanes for.
+constexpr int kJoinRows = 4;  // waves of a workgroup
+template <int DT, int LANES>
+__global__ __launch_bounds__(kJoinRows * 64) void tree_attention_join_kernel(tf_exl3_tree_attention_args a, AttnPlan p, FastDiv by_tile,
+                                                                             int tile_rows) {
+  constexpr int kSlices = 64 / LANES;
+  const int b = blockIdx.y, row = blockIdx.x * kJoinRows + (threadIdx.x >> 6), lane = threadIdx.x & 63;  // row: (head, row of it)
   if (row >= a.kv_heads * p.rows) return;
-  const int2 seq = p.seq[b];
-  if (seq.y == 1) return;
-  const int64_t first = (int64_t)seq.x * a.kv_heads * p.rows + row, step = (int64_t)a.kv_heads * p.rows;
-  float top = -INFINITY;
-  for (int i = 0; i < seq.y; ++i) top = fmaxf(top, p.stat[first + i * step].x);
-  float z = 0.f;
+  const int g = p.by_rows.div(row), r = row - g * p.rows, tile = by_tile.div(r);
+  const SeqTiles seq = p.seq[b];
+  const int64_t begin = seq.begin + (int64_t)(g * p.row_tiles + tile) * seq.tiles;
+  const int64_t from = divide(begin, seq.piece);
+  const int pieces = (int)(divide(begin + seq.tiles - 1, seq.piece) - from) + 1;
+  if (pieces == 1) return;
+  // The first piece may have begun with another group; the others begin with this one.
+  const int64_t head = (from * 2 + (begin > from * seq.piece)) * tile_rows + r - tile * tile_rows;
+  const int64_t next = from * 2 * tile_rows + r - tile * tile_rows, step = 2 * tile_rows;
+  auto at = [&](int i) { return i == 0 ? head : next + i * step; };
+  const int slice = lane / LANES, d = lane % LANES * 4;
+  float top = -INFINITY, z = 0.f;
   f32x4 o = f32x4(0.f);
-  for (int i = 0; i < seq.y; ++i) {
-    const float2 st = p.stat[first + i * step];
-    const float w = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.x - top);
-    z = __builtin_fmaf(st.y, w, z);
-    o += *reinterpret_cast<const f32x4*>(p.part + (first + i * step) * a.head_dim + d) * w;
+  for (int r0 = 0; r0 < pieces; r0 += 64) {
+    float2 st = make_float2(-INFINITY, 0.f);
+    if (r0 + lane < pieces) st = p.stat[at(r0 + lane)];
+    const float grown = fmaxf(top, wave_max(st.x));
+    const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - grown);
+    const float w = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.x - grown);
+    top = grown;
+    z = z * keep + wave_sum(w * st.y);
+    o *= keep;
+    const int here = min(64, pieces - r0);
+#pragma unroll 4
+    for (int i = 0; i < here; i += kSlices) {
+      const int mine = i + slice;
+      const float wi = __shfl(w, mine < here ? mine : 0);
+      if (mine < here && d < a.head_dim) o += *reinterpret_cast<const f32x4*>(p.part + at(r0 + mine) * a.head_dim + d) * wi;
+    }
   }
-  const int g = row / p.rows, r = row - g * p.rows, node = p.by_group.div(r), head = g * p.group + r - node * p.group;
-  uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + node * a.out_stride[1] + head * a.out_stride[2] + d;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int s = LANES; s < 64; s <<= 1) o[c] += __shfl_xor(o[c], s);
+  if (slice > 0 || d >= a.head_dim) return;
   if (z == 0.f)
     o = f32x4(0.f);
   else
     o *= 1.f / z;
+  const int node = p.by_group.div(r), h = g * p.group + r - node * p.group;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + b * a.out_stride[0] + node * a.out_stride[1] + h * a.out_stride[2] + d;
   *reinterpret_cast<u32x2*>(out) = u32x2{pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3])};
 }
 
@@ -530,6 +627,7 @@ namespace {
 // How a call's rows and positions are spread; by the sizes alone.
 struct Shape {
   int dp, rt, rg, kg, kw;
+  int resident;  // workgroups that a CU holds
   int tile() const { return kg * kw; }
   int rows() const { return 16 * rt * rg; }
 };
@@ -537,11 +635,12 @@ struct Shape {
 Shape shape_of(int dim, int rows) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   // (A wave of one row group holds 32 positions at 256 columns in half its registers.)
-  if (rows <= 16 && dp < 256) return {dp, 1, 1, 2, 32};
-  if (rows <= 32) return {dp, 1, 2, 2, 32};
-  if (rows <= 64 || dp == 256) return {dp, 1, 4, 1, 64};
+  if (rows <= 16 && dp < 256) return {dp, 1, 1, 2, 32, 4};
+  if (rows <= 32) return {dp, 1, 2, 2, 32, 2};
+  if (dp == 256) return {dp, 1, 4, 1, 32, 1};
+  if (rows <= 64) return {dp, 1, 4, 2, 32, 1};
   const int two = (rows + 127) / 128 * 2, three = (rows + 191) / 192 * 3;  // row tiles of 64 that are computed
-  return {dp, two < three ? 2 : 3, 4, 2, 32};
+  return {dp, two < three ? 2 : 3, 4, 2, 32, 1};
 }
 
 constexpr int kCUs = 256;
@@ -559,42 +658,45 @@ Layout layout_of(const tf_exl3_tree_attention_args& a) {
   AttnPlan& p = l.p;
   p.rows = rows, p.group = group;
   p.row_tiles = (rows + l.s.rows() - 1) / l.s.rows();
-  const int64_t room = (int64_t)a.table_pages * a.page_size + a.nodes;
-  const int64_t groups = (int64_t)a.kv_heads * p.row_tiles;  // workgroups of a run
-  // Runs enough for every CU to have as many workgroups as fit it, but none so short that
-  // writing and joining its rows would cost as much as reading its positions.
-  const int64_t slots = kCUs * (l.s.rt > 1 ? 1 : 4);
-  p.min_tiles = l.s.rt > 1 ? 8 : 1;
-  const int64_t run = (int64_t)p.min_tiles * l.s.tile(), most = a.batch * ((room + run - 1) / run);
-  const int64_t target = (slots + groups - 1) / groups;
-  p.target = (int)(target < most ? target : most);
-  if (a.batch > 1024 || p.target <= a.batch / 4 || room <= run) p.target = 0;
-  p.units = a.batch + p.target;
-  const size_t n = p.target ? (size_t)p.units * a.kv_heads * rows : 0;
-  l.seq_bytes = ((size_t)a.batch * sizeof(int2) + 15) / 16 * 16;
+  p.groups = a.kv_heads * p.row_tiles;
+  // A piece is never so short that writing and joining its rows costs as much as its positions.
+  p.min_piece = l.s.rt > 1 ? 4 : 1;
+  const int64_t room = (int64_t)a.table_pages * a.page_size + a.nodes, most = a.batch * ((room + l.s.tile() - 1) / l.s.tile()) * p.groups;
+  const int64_t pieces = (most + p.min_piece - 1) / p.min_piece, slots = kCUs * l.s.resident;
+  p.workgroups = (int)(pieces < slots ? pieces : slots);
+  // Sequences beyond these are many enough to go one by one, and too many for every workgroup
+  // to look through.
+  if (a.batch > 1024) p.workgroups = 0;
+  const size_t n = (size_t)p.workgroups * 2 * l.s.rows();
+  l.seq_bytes = ((size_t)a.batch * sizeof(SeqTiles) + 15) / 16 * 16;
   l.stat_bytes = (n * sizeof(float2) + 15) / 16 * 16;
   l.part_bytes = n * a.head_dim * sizeof(float);
   return l;
 }
 
-template <int DT, int DP, int RT, int RG, int KG, int KW>
+template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int WAVES>
 void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t stream) {
-  const int64_t runs = ((int64_t)p.units * a.kv_heads + 7) / 8 * 8;
-  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW>), dim3((unsigned)(runs * p.row_tiles)), dim3(RG * KG * 64), 0,
-                     stream, AttnArgs{a, p});
+  const unsigned grid = p.workgroups ? (unsigned)p.workgroups : (unsigned)a.batch * (unsigned)p.groups;
+  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW, S, WAVES>), dim3(grid), dim3(RG * KG * 64), 0, stream,
+                     AttnArgs{a, p});
+  if (p.workgroups == 0) return;
+  const int rows = a.kv_heads * p.rows, tile_rows = 16 * RT * RG;
+  hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4>), dim3((rows + kJoinRows - 1) / kJoinRows, a.batch), dim3(kJoinRows * 64),
+                     0, stream, a, p, fast_div(tile_rows), tile_rows);
 }
 
 template <int DT, int DP>
 void launch_dim(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream_t stream) {
   const Shape& s = l.s;
   if constexpr (DP < 256) {
-    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32>(a, l.p, stream);
-  }
-  if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32>(a, l.p, stream);
-  if (s.rt == 1) return launch<DT, DP, 1, 4, 1, 64>(a, l.p, stream);
-  if constexpr (DP < 256) {
-    if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32>(a, l.p, stream);
-    return launch<DT, DP, 3, 4, 2, 32>(a, l.p, stream);
+    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32, 1, 2>(a, l.p, stream);
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 2, 2>(a, l.p, stream);
+    if (s.rt == 1) return launch<DT, DP, 1, 4, 2, 32, 3, 2>(a, l.p, stream);
+    if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32, 1, 2>(a, l.p, stream);
+    return launch<DT, DP, 3, 4, 2, 32, 1, 2>(a, l.p, stream);
+  } else {
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 1>(a, l.p, stream);
+    return launch<DT, DP, 1, 4, 1, 32, 1, 1>(a, l.p, stream);
   }
 }
 
@@ -606,9 +708,6 @@ void launch_type(const tf_exl3_tree_attention_args& a, const Layout& l, hipStrea
     launch_dim<DT, 128>(a, l, stream);
   else
     launch_dim<DT, 256>(a, l, stream);
-  if (l.p.target == 0) return;
-  const int64_t quads = (int64_t)a.kv_heads * l.p.rows * (a.head_dim / 4);
-  hipLaunchKernelGGL(tree_attention_join_kernel<DT>, dim3((unsigned)((quads + 255) / 256), a.batch), dim3(256), 0, stream, a, l.p);
 }
 
 }  // namespace
@@ -620,10 +719,9 @@ size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a) {
 
 hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream) {
   Layout l = layout_of(a);
-  const int64_t runs = ((int64_t)l.p.units * a.kv_heads + 7) / 8 * 8;
-  if (runs * l.p.row_tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  if ((int64_t)a.batch * l.p.groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   char* ws = static_cast<char*>(a.workspace);
-  l.p.seq = reinterpret_cast<int2*>(ws);
+  l.p.seq = reinterpret_cast<SeqTiles*>(ws);
   l.p.stat = reinterpret_cast<float2*>(ws + l.seq_bytes);
   l.p.part = reinterpret_cast<float*>(ws + l.seq_bytes + l.stat_bytes);
   // A scale of 0 keeps masked scores apart from others: the smallest factor does the same to sums.
@@ -631,9 +729,13 @@ hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream
   l.p.c = c > 1.2e-38f ? c : 1.2e-38f;
   l.p.slack = fminf(8.f / l.p.c, 3e38f);
   l.p.negate = a.scale < 0.f;
+  const int64_t page = a.k_cache_stride[0] * 2, slot = a.k_cache_stride[1] * 2;
+  const bool same = a.v_cache_stride[0] * 2 == page && a.v_cache_stride[1] * 2 == slot;
+  l.p.page_bytes = same && page < (1ll << 32) && slot < (1ll << 32) ? (uint32_t)page : 0;
+  l.p.slot_bytes = (uint32_t)slot;
+  l.p.step_cols = l.s.tile() / a.page_size, l.p.step_slots = l.s.tile() % a.page_size;
   l.p.by_group = fast_div(l.p.group), l.p.by_page = fast_div(a.page_size);
-  l.p.by_row_tiles = fast_div(l.p.row_tiles), l.p.by_heads = fast_div(a.kv_heads);
-  l.p.by_quads = fast_div(a.head_dim / 4);
+  l.p.by_row_tiles = fast_div(l.p.row_tiles), l.p.by_rows = fast_div(l.p.rows), l.p.by_groups = fast_div(l.p.groups);
   if (a.dtype == TF_DT_F16)
     launch_type<TF_DT_F16>(a, l, stream);
   else
