@@ -124,6 +124,10 @@ __device__ __forceinline__ float dpp(float v, float rest) {
                                                                ROWS, 0xF, false));
 }
 template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int v, int rest) {
+  return __builtin_amdgcn_update_dpp(rest, v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp(double v, double rest) {
   typedef int i32x2 __attribute__((ext_vector_type(2)));
   const i32x2 a = __builtin_bit_cast(i32x2, v), r = __builtin_bit_cast(i32x2, rest);

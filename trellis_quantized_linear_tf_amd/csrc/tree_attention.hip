@@ -82,6 +82,9 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// Matrix products and reads of shared memory stay on their side; other work may cross.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x2 | 0x4 | 0x10); }
+
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (DT == TF_DT_F16) {
@@ -128,28 +131,37 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // A stretch of one group's tiles.
 struct Segment {
   int b, group, tile, left;  // left: tiles of the piece from here on
+  int len;                   // of the sequence in the cache
   int64_t begin;             // of the sequence in the line
   int piece;
 };
 
-template <int KT>
-__device__ __forceinline__ int tiles_of(ArgPtr x, int b) { return (cached(x, b) + x->a.nodes + KT - 1) / KT; }
-
-// Where the workgroup's piece begins.
+// Where the workgroup's piece begins. Sequences are looked at 64 at a time, a lane each; the
+// lengths of up to 64 are read once.
 template <int KT>
 __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
-  const int batch = x->a.batch, groups = x->p.groups, workgroups = x->p.workgroups;
+  const int batch = x->a.batch, groups = x->p.groups, workgroups = x->p.workgroups, nodes = x->a.nodes;
   if (workgroups == 0) {
     s->b = copy(&x->p.by_groups).div(w), s->group = w - s->b * groups;
-    s->tile = 0, s->left = uniform(tiles_of<KT>(x, s->b)), s->begin = 0, s->piece = 0;
+    s->len = uniform(cached(x, s->b));
+    s->tile = 0, s->left = (s->len + nodes + KT - 1) / KT, s->begin = 0, s->piece = 0;
     return true;
   }
   const int lane = threadIdx.x & 63;
+  int len = 0, tiles = 0;
+  uint32_t end = 0;  // tiles up to and with the lane's sequence
+  auto look = [&](int b0) {
+    const bool there = b0 + lane < batch;
+    len = there ? cached(x, b0 + lane) : 0;
+    tiles = there ? (len + nodes + KT - 1) / KT : 0;
+    end = (uint32_t)wave_scan(tiles);  // at most 64 times 2^30 positions in tiles of 32: 2^31
+  };
   int64_t all = 0;
-  for (int b = lane; b < batch; b += 64) all += tiles_of<KT>(x, b);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
-  all = uniform(all) * groups;
+  for (int b0 = 0; b0 < batch; b0 += 64) {
+    look(b0);
+    all += (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+  }
+  all *= groups;
   const int64_t even = divide(all + workgroups - 1, workgroups);
   s->piece = uniform((int)(even < x->p.min_piece ? x->p.min_piece : even));
   const int64_t from = (int64_t)w * s->piece;
@@ -157,24 +169,18 @@ __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
   s->left = (int)(all - from < s->piece ? all - from : s->piece);
   int64_t base = 0;
   for (int b0 = 0;; b0 += 64) {
-    const int tiles = b0 + lane < batch ? tiles_of<KT>(x, b0 + lane) : 0;
-    int64_t end = (int64_t)tiles * groups;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t up = __shfl_up(end, o);
-      if (lane >= o) end += up;
-    }
-    end += base;
-    const uint64_t hit = __ballot(end > from);
+    if (batch > 64) look(b0);
+    const uint64_t hit = __ballot((base + end) * groups > from);
     if (hit) {
       const int at = __builtin_ctzll(hit), n = __builtin_amdgcn_readlane(tiles, at);
       s->b = b0 + at;
-      s->begin = uniform(__shfl(end, at)) - (int64_t)n * groups;
+      s->len = __builtin_amdgcn_readlane(len, at);
+      s->begin = (base + (uint32_t)__builtin_amdgcn_readlane((int)end, at) - n) * groups;
       s->group = uniform((int)divide(from - s->begin, n));
       s->tile = (int)(from - s->begin - (int64_t)s->group * n);
       return true;
     }
-    base = uniform(__shfl(end, 63));
+    base += (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
   }
 }
 
@@ -204,12 +210,14 @@ __device__ __forceinline__ bool drop_nonfinite(u32x4& v) {
 // Bits 0 .. 3: whether a row of mask `seen` sees the positions that begin `node` behind the
 // cache's end (before it where negative), `left` before the run's.
 __device__ __forceinline__ uint32_t seen_of(uint64_t seen, int node, int left) {
-  const uint32_t tree = node >= 0 ? (uint32_t)(seen >> min(node, 63)) : ((uint32_t)seen << min(-node, 4)) | ((1u << min(-node, 4)) - 1);
+  const int before = min(-node, 4);
+  const uint32_t tree = node >= 0 ? (uint32_t)(seen >> min(node, 63)) : ((uint32_t)seen << before) | ((1u << before) - 1);
   return tree & (left >= 4 ? 15u : left <= 0 ? 0u : (1u << left) - 1);
 }
 
-// S: tiles whose keys and values are on their way to registers.
-template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int WAVES>
+// S: tiles whose keys and values are on their way to registers. BUF: tiles in shared memory;
+// with two of them a tile is put there while the one before is still in use.
+template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int BUF, int WAVES>
 __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(AttnArgs) {
   typedef uint16_t T;
   constexpr int kThreads = RG * KG * 64, KT = KG * KW, NC = DP / 8, NK = KW / 16, NB = KW / 32, ND = DP / 16, NQ = DP / 32;
@@ -217,7 +225,7 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
   static_assert(KT % kStep == 0 && KW % 32 == 0, "");
   constexpr int kTile = KT * NC;
   constexpr int kJoin = KG > 1 ? (KG - 1) * RG * ND * 64 : 0;  // other key groups' outputs, one row tile at a time
-  __shared__ u32x4 lds[2 * kTile > kJoin ? 2 * kTile : kJoin];
+  __shared__ u32x4 lds[2 * BUF * kTile > kJoin ? 2 * BUF * kTile : kJoin];
   __shared__ float2 join_stat[KG > 1 ? (KG - 1) * RG * 64 : 1];
   __shared__ int odd_values;
 
@@ -228,344 +236,369 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
   const int rg = wave % RG, kg = wave / RG;
   bool first = true;
   for (;;) {
-  x = arguments();
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));  // what depends on it is worked out again and not kept over segments
-  const int lane = tid & 63, lg = lane >> 4;
-  const int nodes = x->a.nodes, b = seg.b;
-  const int g = copy(&x->p.by_row_tiles).div(seg.group), row_tile = seg.group - g * x->p.row_tiles;
-  const int len = uniform(cached(x, b)), tiles = (len + nodes + KT - 1) / KT;
-  const int begin = seg.tile * KT, until = min(tiles, seg.tile + seg.left);
-  const int stop = min(until * KT, len + nodes);  // positions of the segment: begin .. stop - 1
-  const bool whole = seg.tile == 0 && until == tiles;
-  if (x->p.workgroups && seg.group == 0 && seg.tile == 0 && tid == 0) x->p.seq[b] = {seg.begin, tiles, seg.piece};
-  if (tid == 0) odd_values = 0;
+    x = arguments();
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));  // what depends on it is worked out again and not kept over segments
+    const int lane = tid & 63, lg = lane >> 4;
+    const int nodes = x->a.nodes, b = seg.b;
+    const int g = copy(&x->p.by_row_tiles).div(seg.group), row_tile = seg.group - g * x->p.row_tiles;
+    const int len = seg.len, tiles = (len + nodes + KT - 1) / KT;
+    const int begin = seg.tile * KT, until = min(tiles, seg.tile + seg.left);
+    const int stop = min(until * KT, len + nodes);  // positions of the segment: begin .. stop - 1
+    const bool whole = seg.tile == 0 && until == tiles;
+    if (x->p.workgroups && seg.group == 0 && seg.tile == 0 && tid == 0) x->p.seq[b] = {seg.begin, tiles, seg.piece};
+    if (tid == 0) odd_values = 0;
 
-  // The rows' queries and masks.
-  const int row0 = (row_tile * RG + rg) * 16 * RT;
-  const bool active = row0 < x->p.rows;
-  u32x4 q[RT][NQ];
-  uint64_t seen[RT];
-  {
-    const int rows = x->p.rows, group = x->p.group, dim = x->a.head_dim;
-    const FastDiv by_group = copy(&x->p.by_group);
-    const uint32_t flip = x->p.negate ? 0x80008000u : 0u;
+    // The rows' queries and masks.
+    const int row0 = (row_tile * RG + rg) * 16 * RT;
+    const bool active = row0 < x->p.rows;
+    u32x4 q[RT][NQ];
+    uint64_t seen[RT];
+    {
+      const int rows = x->p.rows, group = x->p.group, dim = x->a.head_dim;
+      const FastDiv by_group = copy(&x->p.by_group);
+      const uint32_t flip = x->p.negate ? 0x80008000u : 0u;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int r = row0 + rt * 16 + (lane & 15), have = min(r, rows - 1);
+        const int node = by_group.div(have), head = g * group + have - node * group;
+        const T* row = static_cast<const T*>(x->a.q) + b * x->a.q_stride[0] + node * x->a.q_stride[1] + head * x->a.q_stride[2];
+        seen[rt] = r < rows ? (uint64_t)x->a.mask[(int64_t)b * nodes + node] : 0;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const int d = i * 32 + lg * 8;
+          q[rt][i] = u32x4(0u);
+          if (r < rows && d < dim) q[rt][i] = *reinterpret_cast<const u32x4*>(row + d);
+          q[rt][i] ^= flip;
+        }
+      }
+    }
+
+    // The loader's part: chunk `chunk` of rows tid / NC, + kStep, ...
+    const int chunk = tid % NC, lrow = tid / NC;
+    x = arguments();
+    const float scale_c = x->p.c, slack = x->p.slack;
+    const bool have = chunk * 8 < x->a.head_dim;
+    const T* kc = static_cast<const T*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * 8;
+    const T* vc = static_cast<const T*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * 8;
+    const uint32_t page_bytes = x->p.page_bytes, slot_bytes = x->p.slot_bytes;  // page_bytes 0: wide or different strides
+    const int32_t* table = x->a.table + b * x->a.table_stride;
+    const int pages = x->a.pages, page_size = x->a.page_size;
+    const int step_cols = x->p.step_cols, step_slots = x->p.step_slots;
+    u32x4 kr[S][kLoads], vr[S][kLoads];
+    // A row's page and slot go on by a tile at a time; rows behind the cache's end look at its
+    // last page, which is there, and are not used.
+    int page[kLoads] = {}, col[kLoads], slot[kLoads];
+    const FastDiv by_page = copy(&x->p.by_page);
+    const int last_col = len > 0 ? by_page.div(len - 1) : 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int j = begin + lrow + i * kStep;
+      col[i] = by_page.div(j);
+      slot[i] = j - col[i] * page_size;
+    }
+    auto look_up = [&]() {
+      if (len > 0) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) page[i] = *reinterpret_cast<const int32_t*>(
+            reinterpret_cast<const char*>(table) + (uint32_t)min(col[i], last_col) * 4u);
+      }
+    };
+    auto advance = [&]() {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        slot[i] += step_slots, col[i] += step_cols;
+        const bool wrap = slot[i] >= page_size;
+        slot[i] -= wrap ? page_size : 0, col[i] += wrap;
+      }
+    };
+    auto load = [&](int at, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads]) {
+      const bool edge = at + KT > min(len, stop);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t pg = (uint32_t)page[i] < (uint32_t)pages ? page[i] : 0;
+        const T *kp, *vp;
+        if (page_bytes) {
+          const uint64_t off = (uint64_t)pg * page_bytes + (uint64_t)(uint32_t)slot[i] * slot_bytes;
+          kp = reinterpret_cast<const T*>(reinterpret_cast<const char*>(kc) + off);
+          vp = reinterpret_cast<const T*>(reinterpret_cast<const char*>(vc) + off);
+        } else {
+          const ArgPtr y = arguments();
+          kp = kc + pg * y->a.k_cache_stride[0] + slot[i] * y->a.k_cache_stride[1];
+          vp = vc + pg * y->a.v_cache_stride[0] + slot[i] * y->a.v_cache_stride[1];
+        }
+        if (edge) {
+          const ArgPtr y = arguments();
+          const int j = at + lrow + i * kStep, node = min(j, stop - 1) - len;  // behind the run's end its last row again
+          const T* kt = static_cast<const T*>(y->a.k) + b * y->a.k_stride[0] + node * y->a.k_stride[1] + g * y->a.k_stride[2];
+          const T* vt = static_cast<const T*>(y->a.v) + b * y->a.v_stride[0] + node * y->a.v_stride[1] + g * y->a.v_stride[2];
+          kp = j < len ? kp : kt + chunk * 8;
+          vp = j < len ? vp : vt + chunk * 8;
+        }
+        kr[i] = *reinterpret_cast<const u32x4*>(kp);
+        vr[i] = *reinterpret_cast<const u32x4*>(vp);
+      }
+    };
+
+    f32x4 o[ND][RT];
+    float m[RT], z[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int r = row0 + rt * 16 + (lane & 15), have = min(r, rows - 1);
-      const int node = by_group.div(have), head = g * group + have - node * group;
-      const T* row = static_cast<const T*>(x->a.q) + b * x->a.q_stride[0] + node * x->a.q_stride[1] + head * x->a.q_stride[2];
-      seen[rt] = r < rows ? (uint64_t)x->a.mask[(int64_t)b * nodes + node] : 0;
+      m[rt] = -INFINITY, z[rt] = 0.f;
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int d = i * 32 + lg * 8;
-        q[rt][i] = u32x4(0u);
-        if (r < rows && d < dim) q[rt][i] = *reinterpret_cast<const u32x4*>(row + d);
-        q[rt][i] ^= flip;
-      }
+      for (int dt = 0; dt < ND; ++dt) o[dt][rt] = f32x4(0.f);
     }
-  }
+    const int key_row = (kg * KW + (lane & 15)) * NC;
+    const int vrow = lg * 4 + ((lane & 15) >> 2);  // of the 32 positions of a step, and 16 behind
+    const int value_row = kTile + (kg * KW + vrow) * NC;
 
-  // The loader's part: chunk `chunk` of rows tid / NC, + kStep, ...
-  const int chunk = tid % NC, lrow = tid / NC;
-  x = arguments();
-  const float scale_c = x->p.c, slack = x->p.slack;
-  const bool have = chunk * 8 < x->a.head_dim;
-  const T* kc = static_cast<const T*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * 8;
-  const T* vc = static_cast<const T*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * 8;
-  const uint32_t page_bytes = x->p.page_bytes, slot_bytes = x->p.slot_bytes;  // page_bytes 0: wide or different strides
-  const int32_t* table = x->a.table + b * x->a.table_stride;
-  const int pages = x->a.pages, page_size = x->a.page_size;
-  const int step_cols = x->p.step_cols, step_slots = x->p.step_slots;
-  u32x4 kr[S][kLoads], vr[S][kLoads];
-  // A row's page and slot go on by a tile at a time; rows behind the cache's end look at its
-  // last page, which is there, and are not used.
-  int page[kLoads] = {}, col[kLoads], slot[kLoads];
-  const FastDiv by_page = copy(&x->p.by_page);
-  const int last_col = len > 0 ? by_page.div(len - 1) : 0;
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int j = begin + lrow + i * kStep;
-    col[i] = by_page.div(j);
-    slot[i] = j - col[i] * page_size;
-  }
-  auto look_up = [&]() {
-    if (len > 0) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) page[i] = *reinterpret_cast<const int32_t*>(
-          reinterpret_cast<const char*>(table) + (uint32_t)min(col[i], last_col) * 4u);
-    }
-  };
-  auto advance = [&]() {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      slot[i] += step_slots, col[i] += step_cols;
-      const bool wrap = slot[i] >= page_size;
-      slot[i] -= wrap ? page_size : 0, col[i] += wrap;
-    }
-  };
-  auto load = [&](int at, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads]) {
-    const bool edge = at + KT > min(len, stop);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const uint32_t pg = (uint32_t)page[i] < (uint32_t)pages ? page[i] : 0;
-      const T *kp, *vp;
-      if (page_bytes) {
-        const uint64_t off = (uint64_t)pg * page_bytes + (uint64_t)(uint32_t)slot[i] * slot_bytes;
-        kp = reinterpret_cast<const T*>(reinterpret_cast<const char*>(kc) + off);
-        vp = reinterpret_cast<const T*>(reinterpret_cast<const char*>(vc) + off);
-      } else {
-        const ArgPtr y = arguments();
-        kp = kc + pg * y->a.k_cache_stride[0] + slot[i] * y->a.k_cache_stride[1];
-        vp = vc + pg * y->a.v_cache_stride[0] + slot[i] * y->a.v_cache_stride[1];
-      }
-      if (edge) {
-        const ArgPtr y = arguments();
-        const int j = at + lrow + i * kStep, node = min(j, stop - 1) - len;  // behind the run's end its last row again
-        const T* kt = static_cast<const T*>(y->a.k) + b * y->a.k_stride[0] + g * y->a.k_stride[2] + node * y->a.k_stride[1] + chunk * 8;
-        const T* vt = static_cast<const T*>(y->a.v) + b * y->a.v_stride[0] + g * y->a.v_stride[2] + node * y->a.v_stride[1] + chunk * 8;
-        kp = j < len ? kp : kt;
-        vp = j < len ? vp : vt;
-      }
-      kr[i] = *reinterpret_cast<const u32x4*>(kp);
-      vr[i] = *reinterpret_cast<const u32x4*>(vp);
-    }
-  };
-
-  f32x4 o[ND][RT];
-  float m[RT], z[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    m[rt] = -INFINITY, z[rt] = 0.f;
-#pragma unroll
-    for (int dt = 0; dt < ND; ++dt) o[dt][rt] = f32x4(0.f);
-  }
-  const u32x4* key_row = lds + (kg * KW + (lane & 15)) * NC;
-  const int vrow = lg * 4 + ((lane & 15) >> 2);  // of the 32 positions of a step, and 16 behind
-  const u32x4* value_row = lds + kTile + (kg * KW + vrow) * NC;
-
-  if (have) {
-    look_up();
-#pragma unroll
-    for (int st = 0; st < S; ++st) {
-      if (begin + st * KT < stop) load(begin + st * KT, kr[st], vr[st]);
-      advance();
-      look_up();
-    }
-  } else {
-    // Columns behind the head's are zero throughout.
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = lrow + i * kStep;
-      lds[r * NC + key_chunk<DP>(r, chunk)] = u32x4(0u);
-      lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = u32x4(0u);
-    }
-  }
-  for (int at0 = begin; at0 < stop; at0 += S * KT) {
-#pragma unroll
-  for (int st = 0; st < S; ++st) {
-    const int at = at0 + st * KT;
-    if (at >= stop) break;
-    const bool edge = at + KT > min(len, stop);
-    __syncthreads();  // the last tile has been used
-    if (have) {
-      if (edge) {
+    // A tile from its registers into shared memory, and the registers' next one on its way.
+    auto put = [&](int at, u32x4* to, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads]) {
+      if (!have) return;
+      if (at + KT > min(len, stop)) {
         // A node's values that are no numbers would reach the rows that do not see it as 0 times
         // them; they are put back below.
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int j = at + lrow + i * kStep;
-          if (j >= stop) vr[st][i] = u32x4(0u);
-          if (j >= len && drop_nonfinite<DT>(vr[st][i])) odd_values = 1;
+          if (j >= stop) vr[i] = u32x4(0u);
+          if (j >= len && drop_nonfinite<DT>(vr[i])) odd_values = 1;
         }
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = lrow + i * kStep;
-        lds[r * NC + key_chunk<DP>(r, chunk)] = kr[st][i];
-        lds[kTile + r * NC + value_chunk<DP>(r, chunk)] = vr[st][i];
+        to[r * NC + key_chunk<DP>(r, chunk)] = kr[i];
+        to[kTile + r * NC + value_chunk<DP>(r, chunk)] = vr[i];
       }
       if (at + S * KT < stop) {
-        load(at + S * KT, kr[st], vr[st]);
+        load(at + S * KT, kr, vr);
         advance();
         look_up();
       }
+    };
+    if (have) {
+      look_up();
+#pragma unroll
+      for (int st = 0; st < S; ++st) {
+        if (begin + st * KT < stop) load(begin + st * KT, kr[st], vr[st]);
+        advance();
+        look_up();
+      }
+    } else {
+      // Columns behind the head's are zero throughout.
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = lrow + i * kStep;
+#pragma unroll
+        for (int n = 0; n < BUF; ++n) {
+          lds[2 * n * kTile + r * NC + key_chunk<DP>(r, chunk)] = u32x4(0u);
+          lds[(2 * n + 1) * kTile + r * NC + value_chunk<DP>(r, chunk)] = u32x4(0u);
+        }
+      }
     }
     __syncthreads();
-    if (!active) continue;
+    put(begin, lds, kr[0], vr[0]);
+    int half = 0;  // of shared memory, with the tile in use
+    for (int at0 = begin; at0 < stop; at0 += S * KT) {
+#pragma unroll
+      for (int st = 0; st < S; ++st) {
+        const int at = at0 + st * KT;
+        if (at >= stop) break;
+        const bool edge = at + KT > min(len, stop);
+        __syncthreads();  // the tile is there, and with BUF 2 the one before it no longer in use
+        if (active) {
+          const u32x4* tile = lds + half;
+          f32x4 s[NK][RT];
+#pragma unroll
+          for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) s[t][rt] = f32x4(0.f);
+          // Operands are read kAhead products ahead, or a product would wait out the read of its own.
+          constexpr int kAhead = RT == 3 ? 1 : 2, kRing = kAhead + 1;
+          u32x4 kf[kRing];
+          auto key_operand = [&](int n) { return tile[key_row + n % NK * 16 * NC + key_chunk<DP>(lane & 15, n / NK * 4 + lg)]; };
+#pragma unroll
+          for (int n = 0; n < kAhead; ++n) kf[n] = key_operand(n);
+#pragma unroll
+          for (int n = 0; n < NQ * NK; ++n) {
+            if (n + kAhead < NQ * NK) kf[(n + kAhead) % kRing] = key_operand(n + kAhead);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) s[n % NK][rt] = mfma<DT>(kf[n % kRing], q[rt][n / NK], s[n % NK][rt]);
+            keep_order();
+          }
 
-    f32x4 s[NK][RT];
+          if (edge) {
 #pragma unroll
-    for (int t = 0; t < NK; ++t)
+            for (int t = 0; t < NK; ++t) {
+              const int j = at + kg * KW + t * 16 + lg * 4;  // the first of the lane's four
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[t][rt] = f32x4(0.f);
+              for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t bits = seen_of(seen[rt], j - len, stop - j);
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
-#pragma unroll
-      for (int t = 0; t < NK; ++t) {
-        const u32x4 kf = key_row[t * 16 * NC + key_chunk<DP>(lane & 15, i * 4 + lg)];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[t][rt] = mfma<DT>(kf, q[rt][i], s[t][rt]);
-      }
+                for (int i = 0; i < 4; ++i) s[t][rt][i] = (bits >> i) & 1 ? s[t][rt][i] : -INFINITY;
+              }
+            }
+          }
 
-    if (edge) {
+          // The base m of a row's exponents is raised, and its sums scaled, only where a score has
+          // grown past it by a factor of 2^8: probabilities up to that lose nothing in any type here.
+          // Until then a lane looks at its own positions alone.
+          float top[RT];
+          bool grow = false;
 #pragma unroll
-      for (int t = 0; t < NK; ++t) {
-        const int j = at + kg * KW + t * 16 + lg * 4;  // the first of the lane's four
+          for (int rt = 0; rt < RT; ++rt) {
+            top[rt] = s[0][rt][0];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint32_t bits = seen_of(seen[rt], j - len, stop - j);
+            for (int t = 0; t < NK; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[t][rt][i] = (bits >> i) & 1 ? s[t][rt][i] : -INFINITY;
+              for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], s[t][rt][i]);
+            grow = grow || top[rt] > m[rt] + slack;
+          }
+          if (__ballot(grow)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              const float up = fmaxf(m[rt], groups_max(top[rt]));
+              const float keep = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - up) * scale_c);
+              m[rt] = up;
+              z[rt] *= keep;
+#pragma unroll
+              for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
+            }
+          }
+          u32x4 pf[NB][RT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const float mc = m[rt] == -INFINITY ? 0.f : m[rt] * scale_c;
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < NK; ++t) {
+              float e[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], scale_c, -mc));
+                sum += e[i];
+              }
+              pf[t / 2][rt][(t & 1) * 2] = pack2<DT>(e[0], e[1]);
+              pf[t / 2][rt][(t & 1) * 2 + 1] = pack2<DT>(e[2], e[3]);
+            }
+            z[rt] += sum;
+          }
+          u32x4 vf[kRing];
+          auto value_operand = [&](int n) {
+            // chunks 2 dt and 2 dt + 1 of the row, 8 bytes a lane
+            const u32x4* row = tile + value_row + n / ND * 32 * NC + value_chunk<DP>(vrow, n % ND * 2 + ((lane & 3) >> 1));
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row) + (lane & 1)));
+            const s16x4 hi =
+                __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row + 16 * NC) + (lane & 1)));
+            return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+          };
+#pragma unroll
+          for (int n = 0; n < kAhead; ++n) vf[n] = value_operand(n);
+#pragma unroll
+          for (int n = 0; n < NB * ND; ++n) {
+            if (n + kAhead < NB * ND) vf[(n + kAhead) % kRing] = value_operand(n + kAhead);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) o[n % ND][rt] = mfma<DT>(vf[n % kRing], pf[n / ND][rt], o[n % ND][rt]);
+            keep_order();
+          }
+        }
+        if (at + KT < stop) {
+          if (BUF == 1) __syncthreads();
+          half = BUF == 1 ? 0 : 2 * kTile - half;
+          put(at + KT, lds + half, kr[(st + 1) % S], vr[(st + 1) % S]);
         }
       }
     }
 
-    // The base m of a row's exponents is raised, and its sums scaled, only where a score has
-    // grown past it by a factor of 2^8: probabilities up to that lose nothing in any type here.
-    float top[RT];
-    bool grow = false;
+    __syncthreads();
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      float v = s[0][rt][0];
-#pragma unroll
-      for (int t = 0; t < NK; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v = fmaxf(v, s[t][rt][i]);
-      top[rt] = fmaxf(m[rt], groups_max(v));
-      grow = grow || top[rt] > m[rt] + slack;
-    }
-    if (__ballot(grow)) {
+    for (int rt = 0; rt < RT; ++rt) z[rt] = groups_sum(z[rt]);
+    if constexpr (KG > 1) {
+      // Key group 0 takes in the others' rows, in order.
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const float keep = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - top[rt]) * scale_c);
-        m[rt] = top[rt];
-        z[rt] *= keep;
+        __syncthreads();
+        if (kg > 0) {
+          const int w = (kg - 1) * RG + rg;
+          join_stat[w * 64 + lane] = make_float2(m[rt], z[rt]);
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
-      }
-    }
-    u32x4 pf[NB][RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const float mc = m[rt] == -INFINITY ? 0.f : m[rt] * scale_c;
-      float sum = 0.f;
-#pragma unroll
-      for (int t = 0; t < NK; ++t) {
-        float e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], scale_c, -mc));
-          sum += e[i];
+          for (int dt = 0; dt < ND; ++dt) lds[(w * ND + dt) * 64 + lane] = __builtin_bit_cast(u32x4, o[dt][rt]);
         }
-        pf[t / 2][rt][(t & 1) * 2] = pack2<DT>(e[0], e[1]);
-        pf[t / 2][rt][(t & 1) * 2 + 1] = pack2<DT>(e[2], e[3]);
+        __syncthreads();
+        if (kg == 0) {
+#pragma unroll
+          for (int other = 0; other < KG - 1; ++other) {
+            const int w = other * RG + rg;
+            const float2 st = join_stat[w * 64 + lane];
+            const float top = fmaxf(m[rt], st.x);
+            const float mine = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - top) * scale_c);
+            const float its = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.x - top) * scale_c);
+            m[rt] = top;
+            z[rt] = z[rt] * mine + st.y * its;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt)
+              o[dt][rt] = o[dt][rt] * mine + __builtin_bit_cast(f32x4, lds[(w * ND + dt) * 64 + lane]) * its;
+          }
+        }
       }
-      z[rt] += sum;
     }
+    if (kg == 0 && active) {
+      x = arguments();
+      const int dim = x->a.head_dim;
+      if (odd_values) {
+        for (int j = max(len, begin); j < stop; ++j) {
+          const T* row = static_cast<const T*>(x->a.v) + b * x->a.v_stride[0] + g * x->a.v_stride[2] + (j - len) * x->a.v_stride[1];
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb)
+          for (int dt = 0; dt < ND; ++dt) {
+            if (dt * 16 >= dim) continue;
 #pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        // chunks 2 dt and 2 dt + 1 of the row, 8 bytes a lane
-        const u32x4* row = value_row + kb * 32 * NC + value_chunk<DP>(vrow, dt * 2 + ((lane & 3) >> 1));
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row) + (lane & 1)));
-        const s16x4 hi =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row + 16 * NC) + (lane & 1)));
-        const u32x4 vf = __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+            for (int i = 0; i < 4; ++i) {
+              const float v = Elem<DT>::load(row[dt * 16 + lg * 4 + i]), odd = fabsf(v) < INFINITY ? 0.f : v;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) o[dt][rt] = mfma<DT>(vf, pf[kb][rt], o[dt][rt]);
+              for (int rt = 0; rt < RT; ++rt) o[dt][rt][i] += (seen[rt] >> (j - len)) & 1 ? odd : 0.f;
+            }
+          }
+        }
       }
-  }
-  }
 
-  __syncthreads();
+      const int rows = x->p.rows, group = x->p.group;
+      const FastDiv by_group = copy(&x->p.by_group);
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) z[rt] = groups_sum(z[rt]);
-  if constexpr (KG > 1) {
-    // Key group 0 takes in the others' rows, in order.
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      __syncthreads();
-      if (kg > 0) {
-        const int w = (kg - 1) * RG + rg;
-        join_stat[w * 64 + lane] = make_float2(m[rt], z[rt]);
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) lds[(w * ND + dt) * 64 + lane] = __builtin_bit_cast(u32x4, o[dt][rt]);
-      }
-      __syncthreads();
-      if (kg == 0) {
-#pragma unroll
-        for (int other = 0; other < KG - 1; ++other) {
-          const int w = other * RG + rg;
-          const float2 st = join_stat[w * 64 + lane];
-          const float top = fmaxf(m[rt], st.x);
-          const float mine = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - top) * scale_c);
-          const float its = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((st.x - top) * scale_c);
-          m[rt] = top;
-          z[rt] = z[rt] * mine + st.y * its;
+      for (int rt = 0; rt < RT; ++rt) {
+        const int r = row0 + rt * 16 + (lane & 15);
+        if (r >= rows) continue;
+        if (whole) {
+          const int node = by_group.div(r), head = g * group + r - node * group;
+          T* out = static_cast<T*>(x->a.out) + b * x->a.out_stride[0] + node * x->a.out_stride[1] + head * x->a.out_stride[2] + lg * 4;
+          const float inv = z[rt] == 0.f ? 0.f : 1.f / z[rt];
 #pragma unroll
           for (int dt = 0; dt < ND; ++dt)
-            o[dt][rt] = o[dt][rt] * mine + __builtin_bit_cast(f32x4, lds[(w * ND + dt) * 64 + lane]) * its;
+            if (dt * 16 < dim) {
+              const f32x4 v = z[rt] == 0.f ? f32x4(0.f) : o[dt][rt] * inv;
+              *reinterpret_cast<u32x2*>(out + dt * 16) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+            }
+        } else {
+          const int64_t row = ((int64_t)blockIdx.x * 2 + !first) * (16 * RT * RG) + r - row_tile * (16 * RT * RG);
+          if (lg == 0) x->p.stat[row] = make_float2(m[rt] == -INFINITY ? -INFINITY : m[rt] * scale_c, z[rt]);
+          float* part = x->p.part + row * dim + lg * 4;
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt)
+            if (dt * 16 < dim) *reinterpret_cast<f32x4*>(part + dt * 16) = o[dt][rt];
         }
       }
     }
-  }
-  if (kg == 0 && active) {
-  x = arguments();
-  const int dim = x->a.head_dim;
-  if (odd_values) {
-    for (int j = max(len, begin); j < stop; ++j) {
-      const T* row = static_cast<const T*>(x->a.v) + b * x->a.v_stride[0] + g * x->a.v_stride[2] + (j - len) * x->a.v_stride[1];
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) {
-        if (dt * 16 >= dim) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = Elem<DT>::load(row[dt * 16 + lg * 4 + i]), odd = fabsf(v) < INFINITY ? 0.f : v;
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) o[dt][rt][i] += (seen[rt] >> (j - len)) & 1 ? odd : 0.f;
-        }
-      }
-    }
-  }
 
-  const int rows = x->p.rows, group = x->p.group;
-  const FastDiv by_group = copy(&x->p.by_group);
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = row0 + rt * 16 + (lane & 15);
-    if (r >= rows) continue;
-    if (whole) {
-      const int node = by_group.div(r), head = g * group + r - node * group;
-      T* out = static_cast<T*>(x->a.out) + b * x->a.out_stride[0] + node * x->a.out_stride[1] + head * x->a.out_stride[2] + lg * 4;
-      const float inv = z[rt] == 0.f ? 0.f : 1.f / z[rt];
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt)
-        if (dt * 16 < dim) {
-          const f32x4 v = z[rt] == 0.f ? f32x4(0.f) : o[dt][rt] * inv;
-          *reinterpret_cast<u32x2*>(out + dt * 16) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-        }
-    } else {
-      const int64_t row = ((int64_t)blockIdx.x * 2 + !first) * (16 * RT * RG) + r - row_tile * (16 * RT * RG);
-      if (lg == 0) x->p.stat[row] = make_float2(m[rt] == -INFINITY ? -INFINITY : m[rt] * scale_c, z[rt]);
-      float* part = x->p.part + row * dim + lg * 4;
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt)
-        if (dt * 16 < dim) *reinterpret_cast<f32x4*>(part + dt * 16) = o[dt][rt];
+    seg.left -= until - seg.tile;
+    if (seg.left <= 0) return;
+    seg.tile = 0, first = false;
+    if (++seg.group == arguments()->p.groups) {
+      seg.begin += (int64_t)tiles * seg.group;
+      seg.group = 0, ++seg.b;
+      seg.len = uniform(cached(arguments(), seg.b));
     }
-  }
-  }
-
-  seg.left -= until - seg.tile;
-  if (seg.left <= 0) return;
-  seg.tile = 0, first = false;
-  if (++seg.group == arguments()->p.groups) {
-    seg.begin += (int64_t)tiles * seg.group;
-    seg.group = 0, ++seg.b;
-  }
-  __syncthreads();
+    __syncthreads();
   }
 }
 
@@ -605,7 +638,8 @@ __global__ __launch_bounds__(kJoinRows * 64) void tree_attention_join_kernel(tf_
     for (int i = 0; i < here; i += kSlices) {
       const int mine = i + slice;
       const float wi = __shfl(w, mine < here ? mine : 0);
-      if (mine < here && d < a.head_dim) o += *reinterpret_cast<const f32x4*>(p.part + at(r0 + mine) * a.head_dim + d) * wi;
+      if (mine < here && d < a.head_dim)
+        o += *reinterpret_cast<const f32x4*>(p.part + at(r0 + mine) * a.head_dim + d) * wi;
     }
   }
 #pragma unroll
@@ -661,7 +695,8 @@ Layout layout_of(const tf_exl3_tree_attention_args& a) {
   p.groups = a.kv_heads * p.row_tiles;
   // A piece is never so short that writing and joining its rows costs as much as its positions.
   p.min_piece = l.s.rt > 1 ? 4 : 1;
-  const int64_t room = (int64_t)a.table_pages * a.page_size + a.nodes, most = a.batch * ((room + l.s.tile() - 1) / l.s.tile()) * p.groups;
+  const int64_t room = (int64_t)a.table_pages * a.page_size + a.nodes;
+  const int64_t most = a.batch * ((room + l.s.tile() - 1) / l.s.tile()) * p.groups;
   const int64_t pieces = (most + p.min_piece - 1) / p.min_piece, slots = kCUs * l.s.resident;
   p.workgroups = (int)(pieces < slots ? pieces : slots);
   // Sequences beyond these are many enough to go one by one, and too many for every workgroup
@@ -674,29 +709,30 @@ Layout layout_of(const tf_exl3_tree_attention_args& a) {
   return l;
 }
 
-template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int WAVES>
+template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int BUF, int WAVES>
 void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t stream) {
   const unsigned grid = p.workgroups ? (unsigned)p.workgroups : (unsigned)a.batch * (unsigned)p.groups;
-  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW, S, WAVES>), dim3(grid), dim3(RG * KG * 64), 0, stream,
+  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW, S, BUF, WAVES>), dim3(grid), dim3(RG * KG * 64), 0, stream,
                      AttnArgs{a, p});
   if (p.workgroups == 0) return;
   const int rows = a.kv_heads * p.rows, tile_rows = 16 * RT * RG;
-  hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4>), dim3((rows + kJoinRows - 1) / kJoinRows, a.batch), dim3(kJoinRows * 64),
-                     0, stream, a, p, fast_div(tile_rows), tile_rows);
+  const dim3 join((rows + kJoinRows - 1) / kJoinRows, a.batch);
+  hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4>), join, dim3(kJoinRows * 64), 0, stream, a, p, fast_div(tile_rows),
+                     tile_rows);
 }
 
 template <int DT, int DP>
 void launch_dim(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream_t stream) {
   const Shape& s = l.s;
   if constexpr (DP < 256) {
-    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32, 1, 2>(a, l.p, stream);
-    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 2, 2>(a, l.p, stream);
-    if (s.rt == 1) return launch<DT, DP, 1, 4, 2, 32, 3, 2>(a, l.p, stream);
-    if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32, 1, 2>(a, l.p, stream);
-    return launch<DT, DP, 3, 4, 2, 32, 1, 2>(a, l.p, stream);
+    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32, 1, 1, 2>(a, l.p, stream);
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 2, 2, 2>(a, l.p, stream);
+    if (s.rt == 1) return launch<DT, DP, 1, 4, 2, 32, 3, 2, 2>(a, l.p, stream);
+    if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32, 1, 2, 2>(a, l.p, stream);
+    return launch<DT, DP, 3, 4, 2, 32, 1, 1, 2>(a, l.p, stream);
   } else {
-    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 1>(a, l.p, stream);
-    return launch<DT, DP, 1, 4, 1, 32, 1, 1>(a, l.p, stream);
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 2, 1>(a, l.p, stream);
+    return launch<DT, DP, 1, 4, 1, 32, 1, 2, 1>(a, l.p, stream);
   }
 }
 
