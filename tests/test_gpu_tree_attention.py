@@ -154,6 +154,15 @@ def test_long_sequences(gpu, dt, dim, nodes, hq):
     check(case, run(case))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("length", [700, 2100, 2600, 3300, 4500, 6200, 7000, 9000, 12500])
+def test_one_row_over_many_pieces(gpu, dim, length):
+    """Few rows over one sequence: as many workgroups as its tiles allow, joined into each row."""
+    say(f"pieces {dim} {length}")
+    case = Case(length + dim, "bf16", [length], 1, 3, 1, dim, 64)
+    check(case, run(case))
+
+
 def test_many_sequences(gpu):
     case = Case(9, "bf16", [(7 * b) % 50 for b in range(300)], 2, 2, 1, 64, 16)
     check(case, run(case))

@@ -136,6 +136,8 @@ struct Segment {
   int piece;
 };
 
+constexpr int kMostPieces = 96;
+
 // Where the workgroup's piece begins. Sequences are looked at 64 at a time, a lane each; the
 // lengths of up to 64 are read once.
 template <int KT>
@@ -162,8 +164,11 @@ __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
     all += (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
   }
   all *= groups;
-  const int64_t even = divide(all + workgroups - 1, workgroups);
-  s->piece = uniform((int)(even < x->p.min_piece ? x->p.min_piece : even));
+  // Equal pieces, but no more than about kMostPieces of a row, which all have to be joined.
+  int64_t size = divide(all + workgroups - 1, workgroups);
+  const int64_t joined = divide(all, (int64_t)batch * groups * kMostPieces);
+  size = size > joined ? size : joined;
+  s->piece = uniform((int)(size < x->p.min_piece ? x->p.min_piece : size));
   const int64_t from = (int64_t)w * s->piece;
   if (from >= all) return false;
   s->left = (int)(all - from < s->piece ? all - from : s->piece);
@@ -602,14 +607,18 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
   }
 }
 
-// One wave per row: the weights of the pieces that its tiles lie in, a lane each, then their
-// outputs, four columns a lane and as many pieces at a time as the wave has lanes for.
-constexpr int kJoinRows = 4;  // waves of a workgroup
-template <int DT, int LANES>
-__global__ __launch_bounds__(kJoinRows * 64) void tree_attention_join_kernel(tf_exl3_tree_attention_args a, AttnPlan p, FastDiv by_tile,
-                                                                             int tile_rows) {
-  constexpr int kSlices = 64 / LANES;
-  const int b = blockIdx.y, row = blockIdx.x * kJoinRows + (threadIdx.x >> 6), lane = threadIdx.x & 63;  // row: (head, row of it)
+// WAVES waves per row: the weights of the pieces that its tiles lie in, a lane each, then their
+// outputs, four columns a lane and as many pieces at a time as a wave has lanes for. Several
+// waves take every WAVES-th piece each, and the first joins what they have.
+template <int DT, int LANES, int WAVES>
+__global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs args, FastDiv by_tile, int tile_rows) {
+  constexpr int kSlices = 64 / LANES, kRows = 4 / WAVES;
+  __shared__ f32x4 out_part[WAVES > 1 ? WAVES - 1 : 1][LANES];
+  __shared__ float2 stat_part[WAVES];
+  const tf_exl3_tree_attention_args& a = args.a;
+  const AttnPlan& p = args.p;
+  const int wave = uniform((int)threadIdx.x >> 6), sub = wave % WAVES, lane = threadIdx.x & 63;
+  const int b = blockIdx.y, row = blockIdx.x * kRows + wave / WAVES;  // (head, row of it)
   if (row >= a.kv_heads * p.rows) return;
   const int g = p.by_rows.div(row), r = row - g * p.rows, tile = by_tile.div(r);
   const SeqTiles seq = p.seq[b];
@@ -622,31 +631,57 @@ __global__ __launch_bounds__(kJoinRows * 64) void tree_attention_join_kernel(tf_
   const int64_t next = from * 2 * tile_rows + r - tile * tile_rows, step = 2 * tile_rows;
   auto at = [&](int i) { return i == 0 ? head : next + i * step; };
   const int slice = lane / LANES, d = lane % LANES * 4;
+  const bool have = d < a.head_dim;
   float top = -INFINITY, z = 0.f;
   f32x4 o = f32x4(0.f);
-  for (int r0 = 0; r0 < pieces; r0 += 64) {
+  for (int r0 = sub; r0 < pieces; r0 += 64 * WAVES) {
+    const int mine = r0 + lane * WAVES, here = min(64, (pieces - r0 + WAVES - 1) / WAVES);
     float2 st = make_float2(-INFINITY, 0.f);
-    if (r0 + lane < pieces) st = p.stat[at(r0 + lane)];
+    if (lane < here) st = p.stat[at(mine)];
     const float grown = fmaxf(top, wave_max(st.x));
     const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - grown);
     const float w = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.x - grown);
     top = grown;
     z = z * keep + wave_sum(w * st.y);
     o *= keep;
-    const int here = min(64, pieces - r0);
-#pragma unroll 4
-    for (int i = 0; i < here; i += kSlices) {
-      const int mine = i + slice;
-      const float wi = __shfl(w, mine < here ? mine : 0);
-      if (mine < here && d < a.head_dim)
-        o += *reinterpret_cast<const f32x4*>(p.part + at(r0 + mine) * a.head_dim + d) * wi;
+    constexpr int kAhead = 4;  // outputs on their way
+    for (int i0 = 0; i0 < here; i0 += kSlices * kAhead) {  // the same for all lanes, which hold the weights
+      f32x4 v[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kSlices + slice;
+        v[k] = f32x4(0.f);
+        if (have && i < here) v[k] = *reinterpret_cast<const f32x4*>(p.part + at(r0 + i * WAVES) * a.head_dim + d);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * kSlices + slice;
+        const float wi = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((i < here ? i : 0) * 4, __builtin_bit_cast(int, w)));
+        if (i < here) o += v[k] * wi;
+      }
     }
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int s = LANES; s < 64; s <<= 1) o[c] += __shfl_xor(o[c], s);
-  if (slice > 0 || d >= a.head_dim) return;
+  if constexpr (WAVES > 1) {
+    if (lane == 0) stat_part[sub] = make_float2(top, z);
+    if (sub > 0 && slice == 0) out_part[sub - 1][lane % LANES] = o;
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      const float2 st = stat_part[w];
+      const float grown = fmaxf(top, st.x);
+      const float mine = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - grown);
+      const float its = st.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(st.x - grown);
+      top = grown;
+      z = z * mine + st.y * its;
+      o = o * mine + out_part[w - 1][lane % LANES] * its;
+    }
+  }
+  if (slice > 0 || !have) return;
   if (z == 0.f)
     o = f32x4(0.f);
   else
@@ -716,9 +751,13 @@ void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t
                      AttnArgs{a, p});
   if (p.workgroups == 0) return;
   const int rows = a.kv_heads * p.rows, tile_rows = 16 * RT * RG;
-  const dim3 join((rows + kJoinRows - 1) / kJoinRows, a.batch);
-  hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4>), join, dim3(kJoinRows * 64), 0, stream, a, p, fast_div(tile_rows),
-                     tile_rows);
+  const FastDiv by_tile = fast_div(tile_rows);
+  if ((int64_t)rows * a.batch < kCUs * 4)  // too few rows to fill the chip with a wave each
+    hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4, 4>), dim3(rows, a.batch), dim3(256), 0, stream, AttnArgs{a, p}, by_tile,
+                       tile_rows);
+  else
+    hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4, 1>), dim3((rows + 3) / 4, a.batch), dim3(256), 0, stream,
+                       AttnArgs{a, p}, by_tile, tile_rows);
 }
 
 template <int DT, int DP>
