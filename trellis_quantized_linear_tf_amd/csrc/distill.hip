@@ -156,7 +156,8 @@ struct Writer {
   float t;
   uint32_t slots;  // with an entry; 31 stands for all from 31 on
 
-  __device__ __forceinline__ Writer(const Scale& scale, const Teacher<THREADS>& teach, float top_, float z_, float weight, int64_t lo)
+  __device__ __forceinline__ Writer(const Scale& scale, const Teacher<THREADS>& teach, float top_, float z_, float weight,
+                                    int64_t lo)
       : sc(scale), s(teach), top(top_), z(z_), w(teach.none ? 0.f : weight * scale.inv), w_z(w / z_), zero(w == 0.f) {
     first = s.head[threadIdx.x], at = next = -1, t = 0.f, slots = 0;
     if (first >= 0) at = s.at[first], t = s.t[first], next = s.next[first];
@@ -373,9 +374,17 @@ static int parts_of(int dtype, int vocab) {
   return (int)((pieces + kPart - 1) / kPart);
 }
 
-// Rows that one workgroup each leave too few workgroups for the chip are cut.
-constexpr int kFewRows = 128;
-static bool cut(int dtype, int rows, int vocab) { return rows <= kFewRows && parts_of(dtype, vocab) > 2; }
+// Rows are cut where they are long (a workgroup of 1024, alone on its CU, would take one) and
+// together no more than the second launch finds in the caches. Rows of 129280, loss and
+// gradient, cut against whole, us: fp32 16 rows 14.9 / 22.8, 64 17.6 / 26.4, 100 27.6 / 26.9,
+// 256 63 / 52; bf16 16 rows 15.3 / 20.3, 128 21.2 / 25.0, 160 26.8 / 26.0, 256 38 / 30. Rows of
+// 20000 whole 13 / 15 at any number.
+constexpr int kLongRow = 512 * 16;         // pieces
+constexpr int64_t kFewBytes = 40ll << 20;  // of logits
+static bool cut(int dtype, int rows, int vocab) {
+  const int64_t bytes = (int64_t)vocab * (dtype == TF_DT_F32 ? 4 : 2);
+  return bytes / 16 > kLongRow && rows * bytes <= kFewBytes;
+}
 
 template <int DT>
 static void launch(const DistillArgs& a, hipStream_t stream) {
@@ -389,7 +398,7 @@ static void launch(const DistillArgs& a, hipStream_t stream) {
   const dim3 grid(a.rows);
   if (pieces <= 256 * 8)
     hipLaunchKernelGGL((distill_row_kernel<DT, 256, 8>), grid, dim3(256), 0, stream, a);
-  else if (pieces <= 512 * 16)
+  else if (pieces <= kLongRow)
     hipLaunchKernelGGL((distill_row_kernel<DT, 512, 16>), grid, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((distill_row_kernel<DT, 1024, 16>), grid, dim3(1024), 0, stream, a);

@@ -770,7 +770,7 @@ void launch_dim(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream
     if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32, 1, 2, 2>(a, l.p, stream);
     return launch<DT, DP, 3, 4, 2, 32, 1, 1, 2>(a, l.p, stream);
   } else {
-    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 2, 1>(a, l.p, stream);
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 1, 1>(a, l.p, stream);
     return launch<DT, DP, 1, 4, 1, 32, 1, 2, 1>(a, l.p, stream);
   }
 }
