@@ -1,6 +1,7 @@
 // Rows of keys and values into a paged cache, byte for byte. Nothing is computed, so the
 // bytes, read once and written once, are the whole cost: every thread has kCopies
-// independent loads in flight before its first store.
+// independent loads in flight before its first store. 32768 tokens of 8 heads of 128, bf16 keys
+// and values into pages: 268 MB read and written in 57 us, 4.7 TB/s (element by element 107).
 #include "ops_device.hpp"
 #include "ops_launch.hpp"
 
@@ -110,11 +111,13 @@ static void launch(const tf_exl3_cache_append_args& a, hipStream_t stream) {
   AppendPlan p;
   p.row_units = a.head_dim * a.elem_bytes / BYTES;
   p.units = 2 * a.kv_heads * p.row_units;
-  // As many tokens as one round of the threads' copies holds, if the chip is full without
-  // cutting them finer; otherwise one each.
+  // Up to as many tokens as one round of the threads' copies holds, but first 1024 workgroups.
+  // One token each against a full round, us: 64 x 16 tokens of 8 heads of 128 4.0 / 5.5, 4 x 512 5.8 /
+  // 6.1, 4 x 2048 15.5 / 12.2, 4 x 8192 63 / 45; 64 x 128 of one head of 64 8.6 / 4.0.
   const int round = kAppendThreads * kCopies / p.units;
   const int most = round < 1 ? 1 : round < kMaxTokens ? round : kMaxTokens;
-  p.tokens = (int64_t)a.batch * a.tokens / most < 1024 ? 1 : most;
+  const int64_t share = (int64_t)a.batch * a.tokens / 1024;
+  p.tokens = share < 1 ? 1 : share < most ? (int)share : most;
   p.by_units = fast_div(p.units), p.by_row = fast_div(p.row_units);
   p.by_heads = fast_div(a.kv_heads), p.by_page = fast_div(a.page_size);
   hipLaunchKernelGGL(cache_append_kernel<BYTES>, dim3((a.tokens + p.tokens - 1) / p.tokens, a.batch), dim3(kAppendThreads), 0,
