@@ -140,6 +140,23 @@ def test_the_same_place_more_than_once(gpu):
     check(x, index, top, w)
 
 
+@pytest.mark.parametrize("vocab", [13, 20011, 140001])
+@pytest.mark.parametrize("k", [3, 9, 300])
+def test_many_entries_of_few_places(gpu, vocab, k):
+    """Every entry of a row at one of a few places, the last ones of the row among them."""
+    say(f"few places {vocab} {k}")
+    x, index, top, w = inputs(vocab + k, 3, vocab, k, "bf16", "f32", missing=False)
+    g = torch.Generator().manual_seed(k)
+    places = torch.tensor([0, 1, 7, vocab // 2, vocab - 3, vocab - 1])
+    index = places[torch.randint(0, 6, (3, k), generator=g)].to(torch.int32)
+    index[2] = vocab - 1
+    check(x, index, top, w)
+
+
+def test_a_few_very_long_rows(gpu):
+    check(*inputs(31, 2, 3_000_017, 40, "f32"))
+
+
 def test_rows_without_a_teacher_or_weight(gpu):
     x, index, top, w = inputs(6, 5, 700, 8, "bf16")
     index[1] = -1

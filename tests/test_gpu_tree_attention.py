@@ -168,6 +168,57 @@ def test_many_sequences(gpu):
     check(case, run(case))
 
 
+def test_more_sequences_than_are_split(gpu):
+    case = Case(21, "bf16", [(11 * b) % 90 for b in range(1500)], 1, 2, 1, 64, 16)
+    check(case, run(case))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.11, 0.7, 1e-30, -3.0])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_scales(gpu, scale, dt):
+    say(f"scale {scale} {dt}")
+    case = Case(22, dt, [700, 0, 33], 5, 4, 2, 64, 16, spread=0.5)
+    case.scale = scale
+    check(case, run(case))
+
+
+def test_caches_of_different_layouts(gpu):
+    """Keys by [page][slot][head], values by [page][head][slot], and a table that is part of a wider one."""
+    case = Case(23, "bf16", [300, 41, 900], 4, 4, 2, 128, 24)
+    a = case.gpu()
+    a["v_cache"] = a["v_cache"].transpose(1, 2).contiguous().transpose(1, 2)
+    wide = torch.full((3, case.table.shape[1] + 5), 2 ** 31 - 1, dtype=torch.int32, device=gpu)
+    wide[:, : case.table.shape[1]] = a["table"]
+    a["table"] = wide[:, : case.table.shape[1]]
+    check(case, tq.tree_attention(**a, scale=case.scale))
+
+
+def test_pages_four_gib_apart(gpu):
+    case = Case(24, "f16", [20], 3, 4, 2, 64, 16)
+    a = case.gpu()
+    pages, far = a["k_cache"].shape[0], 1 << 31
+    for n in ("k_cache", "v_cache"):
+        small = a[n]
+        big = torch.empty(((pages - 1) * far + small[0].numel(),), dtype=torch.float16, device=gpu)
+        a[n] = big.as_strided(small.shape, (far, *small.stride()[1:]))
+        a[n].copy_(small)
+    check(case, tq.tree_attention(**a, scale=case.scale))
+
+
+def test_no_pages_at_all(gpu):
+    case = Case(25, "bf16", [0, 0], 6, 4, 2, 64, 16)
+    a = case.gpu()
+    a["table"] = torch.empty((2, 0), dtype=torch.int32, device=gpu)
+    a["lengths"] = torch.tensor([9, -9], dtype=torch.int32, device=gpu)  # taken as the table's room: none
+    check(case, tq.tree_attention(**a, scale=case.scale))
+
+
+def test_an_empty_batch(gpu):
+    case = Case(26, "bf16", [5], 2, 4, 2, 64, 16)
+    a = {n: (x if n.endswith("cache") else x[:0]) for n, x in case.gpu().items()}
+    assert tq.tree_attention(**a).shape == (0, 2, 4, 64)
+
+
 @pytest.mark.parametrize("spread", [0.0, 1e-3, 12.0])
 def test_flat_and_peaked_scores(gpu, spread):
     """Scores that are all equal, and scores hundreds apart."""

@@ -116,6 +116,30 @@ def test_many_sequences(gpu):
     assert len(set(want[0].tolist())) == 4  # every outcome occurs
 
 
+@pytest.mark.parametrize("vocab", [2048, 2049, 4100, 131072, 300001])
+def test_ends_of_the_random_numbers(gpu, vocab):
+    """The first and the last place with weight, over one chunk, several, and more than a wave has lanes."""
+    say(f"ends {vocab}")
+    x = torch.full((1, 4, vocab), -float("inf"))
+    x[0, 0, [5, vocab - 1]] = torch.tensor([1.0, 1.5])
+    x[0, 1, vocab // 2 : vocab // 2 + 9] = -2.0
+    x[0, 2] = torch.randn(vocab, generator=torch.Generator().manual_seed(vocab))
+    x[0, 3, vocab - 2] = 0.0
+    tokens, parents = np.zeros((1, 1), np.int32), np.full((1, 1), -1, np.int32)
+    for value in (0.0, float(np.nextafter(np.float32(1), np.float32(0))), 0.37):
+        u = np.full((1, 1), value, np.float32)
+        for i in range(4):
+            for t in (None, np.full(1, 0.5, np.float32), np.zeros(1, np.float32)):
+                check_tree(x[:, i : i + 1].contiguous(), tokens, parents, u, t)
+
+
+def test_an_empty_batch(gpu):
+    x = torch.zeros((0, 3, 50), device=gpu)
+    i, u = torch.zeros((0, 3), dtype=torch.int32, device=gpu), torch.zeros((0, 3), device=gpu)
+    assert [t.shape for t in tq.verify_tree(x, i, i, u)] == [(0, 3), (0,), (0,)]
+    assert [t.shape for t in tq.verify_chain(x, i, torch.zeros((0, 2, 50), device=gpu), u)] == [(0,), (0,)]
+
+
 def test_ties_and_masked_vocabularies(gpu):
     """Equal logits, rows with a few finite places, with none, with +inf and NaN, at every
     temperature, for random numbers at the ends of their range."""

@@ -377,15 +377,17 @@ static int parts_of(int dtype, int vocab) {
 }
 
 // Rows are cut where they are long (a workgroup of 1024, alone on its CU, would take one) and
-// together no more than the second launch finds in the caches. Rows of 129280, loss and
+// either together no more than the second launch finds in the caches, or so few that most
+// CUs would have none. Rows of 129280, loss and
 // gradient, cut against whole, us: fp32 16 rows 14.9 / 22.8, 64 17.6 / 26.4, 100 27.6 / 26.9,
 // 256 63 / 52; bf16 16 rows 15.3 / 20.3, 128 21.2 / 25.0, 160 26.8 / 26.0, 256 38 / 30. Rows of
 // 20000 whole 13 / 15 at any number.
 constexpr int kLongRow = 512 * 16;         // pieces
 constexpr int64_t kFewBytes = 40ll << 20;  // of logits
+constexpr int kFewRows = 64;
 static bool cut(int dtype, int rows, int vocab) {
   const int64_t bytes = (int64_t)vocab * (dtype == TF_DT_F32 ? 4 : 2);
-  return bytes / 16 > kLongRow && rows * bytes <= kFewBytes;
+  return bytes / 16 > kLongRow && (rows <= kFewRows || rows * bytes <= kFewBytes);
 }
 
 template <int DT>
