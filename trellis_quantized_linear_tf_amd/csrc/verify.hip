@@ -51,13 +51,42 @@ __device__ __forceinline__ double pow2_poly(double f) {
   return __builtin_fma(p, f, 1.0);
 }
 
-// For sums: what is below 2^-1000 (-inf and NaN too) counts as that, which no sum with a 1
-// in it can tell from 0. Adding 1.5 2^52 rounds y to the integer n in the low word.
-__device__ __forceinline__ double pow2_sum(double y) {
-  y = fmax(y, -1000.0);
+// For sums, 64 table entries 2^(j / 64), j = 0 .. 63, in shared memory shorten that: with y = (64 n + j
+// + r) / 64, 2^y = 2^n 2^(j / 64) 2^(r / 64), the last by a polynomial of degree 4 (2.4e-15 relative).
+// What is below 2^-1000 (-inf and NaN too) counts as that, which no sum with a 1 in it can tell
+// from 0. Adding 1.5 2^52 rounds 64 y to an integer in the low word; shifted by 14 bits it adds n to the
+// exponent, and j 2^14 which the entries have been lowered by.
+constexpr int kTable = 64;
+
+__device__ __forceinline__ void fill_table(double* table) {
+  if (threadIdx.x < kTable) {
+    u32x2 w = __builtin_bit_cast(u32x2, exp2((double)threadIdx.x / kTable));
+    w[1] -= threadIdx.x << 14;
+    table[threadIdx.x] = __builtin_bit_cast(double, w);
+  }
+  __syncthreads();
+}
+
+// sum + 2^y by y64 = 64 y.
+__device__ __forceinline__ double add_pow2(double sum, double y64, const double* table) {
+  y64 = fmax(y64, -64000.0);
+  const double t = y64 + 0x1.8p52, r = y64 - (t - 0x1.8p52);
+  const uint32_t n = __builtin_bit_cast(u32x2, t)[0];
+  u32x2 w = __builtin_bit_cast(u32x2, table[n % kTable]);
+  w[1] += n << 14;
+  double p = 0x1.3b2ad0385b409p-31;
+  p = __builtin_fma(p, r, 0x1.c6b0c40d8c4e9p-23);
+  p = __builtin_fma(p, r, 0x1.ebfbdff82ac52p-15);
+  p = __builtin_fma(p, r, 0x1.62e42fefa0352p-7);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_fma(__builtin_bit_cast(double, w), p, sum);
+}
+
+// The same for one: what is below 2^-1000 counts as 0.
+__device__ __forceinline__ double pow2_or_0(double y) {
+  if (!(y > -1000.0)) return 0.0;
   const double t = y + 0x1.8p52;
-  const double p = pow2_poly(y - (t - 0x1.8p52));
-  u32x2 w = __builtin_bit_cast(u32x2, p);
+  u32x2 w = __builtin_bit_cast(u32x2, pow2_poly(y - (t - 0x1.8p52)));
   w[1] += __builtin_bit_cast(u32x2, t)[0] << 20;
   return __builtin_bit_cast(double, w);
 }
@@ -132,16 +161,24 @@ __device__ __forceinline__ const typename Elem<DT>::type* row_of(const VerifyArg
   return static_cast<const typename Elem<DT>::type*>(a.logits) + b * a.stride_batch + i * a.stride_node;
 }
 
-// One wave per chunk of every row. Bound by the fp64 rate: some 19 full-rate operations
-// a logit against 2 or 4 bytes: 768 rows of 129280 bf16 62 us, 98% of the cycles issue vector
-// instructions; 512 rows of fp32 48 us, 5.5 TB/s.
+// One wave per chunk of every row. Bound by the fp64 rate: some 17 full-rate operations
+// a logit against 2 or 4 bytes: 768 rows of 129280 bf16 57 us (by a polynomial of degree 9 and no
+// table 62, with 98% of the cycles issuing vector instructions); 512 rows of fp32 43 us, 6.1 TB/s.
+// Workgroups of 8 or 16 waves, or several chunks a wave, share the table more and measured
+// 58 to 63 us.
 template <int DT>
 __global__ __launch_bounds__(kWaves * 64) void chunk_kernel(VerifyArgs a, int chunks) {
+  __shared__ double table[kTable];
   const int64_t id = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6), row = id / chunks;
-  if (row >= (int64_t)a.batch * a.nodes) return;
+  const bool there = row < (int64_t)a.batch * a.nodes;
   const int b = (int)(row / a.nodes), chunk = (int)(id - row * chunks);
   float x[kLane];
-  load_chunk<DT>(row_of<DT>(a, b, (int)(row - (int64_t)b * a.nodes)), (int64_t)chunk * kChunk, a.vocab, x);
+  // fp32 rows are bound by their bytes and are on their way before the table is made (43 us against
+  // 45 in the case above); 16-bit rows by their instructions, and kept longer they cost more (61 against 57).
+  if (DT != TF_DT_F32) fill_table(table);
+  if (there) load_chunk<DT>(row_of<DT>(a, b, (int)(row - (int64_t)b * a.nodes)), (int64_t)chunk * kChunk, a.vocab, x);
+  if (DT == TF_DT_F32) fill_table(table);
+  if (!there) return;
   float top = x[0];
 #pragma unroll
   for (int i = 1; i < kLane; ++i) top = fmaxf(top, x[i]);
@@ -150,10 +187,9 @@ __global__ __launch_bounds__(kWaves * 64) void chunk_kernel(VerifyArgs a, int ch
   double sum = 0.0;
   if (t > 0.f && top > -INFINITY) {
     if (top < INFINITY) {
-      const double s = log2_scale(t), m = top;
-      sum = pow2_sum(((double)x[0] - m) * s);
+      const double s = log2_scale(t) * kTable, m = top;
 #pragma unroll
-      for (int i = 1; i < kLane; ++i) sum += pow2_sum(((double)x[i] - m) * s);
+      for (int i = 0; i < kLane; ++i) sum = add_pow2(sum, ((double)x[i] - m) * s, table);
     } else {
 #pragma unroll
       for (int i = 0; i < kLane; ++i) sum += x[i] == top ? 1.0 : 0.0;
@@ -421,7 +457,7 @@ __global__ __launch_bounds__(kChainWaves * 64) void chain_kernel(VerifyArgs a, i
         const u32x4 v = load_piece(q + j + h);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const double y = ((double)x[h + c] - m) * s, w = y > -1000.0 ? pow2_sum(y) : 0.0;
+          const double y = ((double)x[h + c] - m) * s, w = pow2_or_0(y);
           const double d = w * inv - (double)bits_to_f32(v[c]);
           sum += d > 0.0 ? d : 0.0;
         }
