@@ -744,8 +744,12 @@ Layout layout_of(const tf_exl3_tree_attention_args& a) {
   const int64_t pieces = (most + p.min_piece - 1) / p.min_piece, slots = kCUs * l.s.resident;
   p.workgroups = (int)(pieces < slots ? pieces : slots);
   // Sequences beyond these are many enough to go one by one, and too many for every workgroup
-  // to look through.
-  if (a.batch > 1024) p.workgroups = 0;
+  // to look through. A few tiles take one workgroup no longer than two launches take. Whole
+  // against cut, us on the GPU: one sequence of 8 heads, 1 to 4 tiles 6.6 to 10.3 / 8.8 to 10.7, 6 tiles 12.9 /
+  // 10.8; 16 sequences, 4 tiles 9.6 / 15.7, 8 tiles 15.3 / 18.7, 16 tiles 24.4 / 23.7; 16 of 2 heads, 8 tiles
+  // 10.4 / 10.7, 12 tiles 13.4 / 11.6.
+  const int64_t tiles = (room + l.s.tile() - 1) / l.s.tile();
+  if (a.batch > 1024 || tiles <= 4 || (tiles <= 8 && (int64_t)a.batch * p.groups >= 32)) p.workgroups = 0;
   const size_t n = (size_t)p.workgroups * 2 * l.s.rows();
   l.seq_bytes = ((size_t)a.batch * sizeof(SeqTiles) + 15) / 16 * 16;
   l.stat_bytes = (n * sizeof(float2) + 15) / 16 * 16;
