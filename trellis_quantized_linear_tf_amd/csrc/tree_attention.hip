@@ -16,7 +16,7 @@
 // unit in the last place each, which the sum of fp32 probabilities does not see).
 //
 // All tiles of all sequences, heads and row tiles stand in one line, which the workgroups,
-// as many as the chip holds at a time, cut into equal pieces, whatever the lengths are:
+// as many as the chip holds at a time, cut into pieces of equal time, whatever the lengths are:
 // every workgroup finds its piece from the lengths on the device. Where a piece ends within a
 // sequence's tiles, it leaves fp32 outputs with their base and sum, and a second kernel
 // joins them.
@@ -25,7 +25,7 @@
 // heads over 8 of 128, bf16: 2.14 GB in 392 us, 5.5 TB/s (keys and values two or three tiles
 // ahead, 64 to 128 KB a CU; with one tile ahead 496 us). Many rows a key: bound by the vector
 // and matrix instructions, whose times add on this chip: 4 trees of 64 nodes, 48 heads over
-// 8, up to 8191 positions: 70 us, 460 TFLOP/s; of its tile's time about 0.3 are matrix
+// 8, up to 8191 positions: 66 us, 490 TFLOP/s; of its tile's time about 0.3 are matrix
 // products, 0.35 exponentials and sums, 0.2 shared memory, the rest barriers and loads. Taking
 // one row tile's exponentials between another's products, two row tiles a wave, or
 // independent workgroups of half the size measured 3 to 10% slower.
@@ -43,10 +43,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// Where a sequence's tiles begin in the line of all of them, and how many one row tile has.
+// Where a sequence begins in the line, and how many tiles each of its groups has there,
+// behind `start` places that stand for what it costs to begin one.
 struct SeqTiles {
   int64_t begin;
-  int tiles, piece;  // piece: tiles of a workgroup
+  int tiles, start, piece;  // piece: places of a workgroup
 };
 
 struct AttnPlan {
@@ -137,15 +138,19 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
 }
 
-// A stretch of one group's tiles.
+// A stretch of one group's places in the line.
 struct Segment {
-  int b, group, tile, left;  // left: tiles of the piece from here on
-  int len;                   // of the sequence in the cache
-  int64_t begin;             // of the sequence in the line
-  int piece;
+  int b, group, place, left;  // place: in the group; left: places of the piece from here on
+  int len;                    // of the sequence in the cache
+  int64_t begin;              // of the sequence in the line
+  int start, piece;           // as in SeqTiles
 };
 
 constexpr int kMostPieces = 96;
+// Tiles' worth of time to begin a group (queries, page numbers and the first tile, one behind the
+// other; its rows written). With equal tiles the workgroups with two groups ended last: 64-node trees 72.8
+// us against 69.1, 8 sequences of 16 nodes over 3000 positions 34.0 against 32.4.
+constexpr int kStart = 4;
 
 // Where the workgroup's piece begins. Sequences are looked at 64 at a time, a lane each; the
 // lengths of up to 64 are read once.
@@ -155,7 +160,7 @@ __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
   if (workgroups == 0) {
     s->b = copy(&x->p.by_groups).div(w), s->group = w - s->b * groups;
     s->len = uniform(cached(x, s->b));
-    s->tile = 0, s->left = (s->len + nodes + KT - 1) / KT, s->begin = 0, s->piece = 0;
+    s->place = 0, s->left = (s->len + nodes + KT - 1) / KT, s->begin = 0, s->start = s->piece = 0;
     return true;
   }
   const int lane = threadIdx.x & 63;
@@ -172,29 +177,31 @@ __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
     look(b0);
     all += (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
   }
-  all *= groups;
   // Equal pieces, but no more than about kMostPieces of a row, which all have to be joined.
+  const int64_t even = divide(all * groups, workgroups), joined = divide(all, (int64_t)batch * kMostPieces);
+  const int start = uniform((int)(even / 4 < kStart ? even / 4 : kStart));
+  all = (all + (int64_t)batch * start) * groups;
   int64_t size = divide(all + workgroups - 1, workgroups);
-  const int64_t joined = divide(all, (int64_t)batch * groups * kMostPieces);
   size = size > joined ? size : joined;
   s->piece = uniform((int)(size < x->p.min_piece ? x->p.min_piece : size));
+  s->start = start;
   const int64_t from = (int64_t)w * s->piece;
   if (from >= all) return false;
   s->left = (int)(all - from < s->piece ? all - from : s->piece);
   int64_t base = 0;
   for (int b0 = 0;; b0 += 64) {
     if (batch > 64) look(b0);
-    const uint64_t hit = __ballot((base + end) * groups > from);
+    const uint64_t hit = __ballot((base + end + (int64_t)(lane + 1) * start) * groups > from);
     if (hit) {
-      const int at = __builtin_ctzll(hit), n = __builtin_amdgcn_readlane(tiles, at);
+      const int at = __builtin_ctzll(hit), n = __builtin_amdgcn_readlane(tiles, at) + start;
       s->b = b0 + at;
       s->len = __builtin_amdgcn_readlane(len, at);
-      s->begin = (base + (uint32_t)__builtin_amdgcn_readlane((int)end, at) - n) * groups;
+      s->begin = (base + (uint32_t)__builtin_amdgcn_readlane((int)end, at) + (int64_t)(at + 1) * start - n) * groups;
       s->group = uniform((int)divide(from - s->begin, n));
-      s->tile = (int)(from - s->begin - (int64_t)s->group * n);
+      s->place = (int)(from - s->begin - (int64_t)s->group * n);
       return true;
     }
-    base += (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    base += (uint32_t)__builtin_amdgcn_readlane((int)end, 63) + 64ll * start;
   }
 }
 
@@ -257,10 +264,13 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
     const int nodes = x->a.nodes, b = seg.b;
     const int g = copy(&x->p.by_row_tiles).div(seg.group), row_tile = seg.group - g * x->p.row_tiles;
     const int len = seg.len, tiles = (len + nodes + KT - 1) / KT;
-    const int begin = seg.tile * KT, until = min(tiles, seg.tile + seg.left);
+    const int last_place = min(tiles + seg.start, seg.place + seg.left);
+    const int tile = max(0, seg.place - seg.start), until = last_place - seg.start;
+    if (until <= 0) return;  // the piece ends before the group's first tile
+    const int begin = tile * KT;
     const int stop = min(until * KT, len + nodes);  // positions of the segment: begin .. stop - 1
-    const bool whole = seg.tile == 0 && until == tiles;
-    if (x->p.workgroups && seg.group == 0 && seg.tile == 0 && tid == 0) x->p.seq[b] = {seg.begin, tiles, seg.piece};
+    const bool whole = tile == 0 && until == tiles;
+    if (x->p.workgroups && seg.group == 0 && tile == 0 && tid == 0) x->p.seq[b] = {seg.begin, tiles, seg.start, seg.piece};
     if (tid == 0) odd_values = 0;
 
     // The rows' queries and masks.
@@ -604,11 +614,11 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
       }
     }
 
-    seg.left -= until - seg.tile;
+    seg.left -= last_place - seg.place;
     if (seg.left <= 0) return;
-    seg.tile = 0, first = false;
+    seg.place = 0, first = false;
     if (++seg.group == arguments()->p.groups) {
-      seg.begin += (int64_t)tiles * seg.group;
+      seg.begin += (int64_t)(tiles + seg.start) * seg.group;
       seg.group = 0, ++seg.b;
       seg.len = uniform(cached(arguments(), seg.b));
     }
@@ -631,9 +641,9 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs args,
   if (row >= a.kv_heads * p.rows) return;
   const int g = p.by_rows.div(row), r = row - g * p.rows, tile = by_tile.div(r);
   const SeqTiles seq = p.seq[b];
-  const int64_t begin = seq.begin + (int64_t)(g * p.row_tiles + tile) * seq.tiles;
-  const int64_t from = divide(begin, seq.piece);
-  const int pieces = (int)(divide(begin + seq.tiles - 1, seq.piece) - from) + 1;
+  const int64_t begin = seq.begin + (int64_t)(g * p.row_tiles + tile) * (seq.tiles + seq.start);
+  const int64_t from = divide(begin + seq.start, seq.piece);
+  const int pieces = (int)(divide(begin + seq.start + seq.tiles - 1, seq.piece) - from) + 1;
   if (pieces == 1) return;
   // The first piece may have begun with another group; the others begin with this one.
   const int64_t head = (from * 2 + (begin > from * seq.piece)) * tile_rows + r - tile * tile_rows;
