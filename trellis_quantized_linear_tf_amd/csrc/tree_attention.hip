@@ -513,7 +513,8 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
             // chunks 2 dt and 2 dt + 1 of the row, 8 bytes a lane
             const u32x4* row = tile + value_row + n / ND * 32 * NC + value_chunk<DP>(vrow, n % ND * 2 + ((lane & 3) >> 1));
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row) + (lane & 1)));
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4*)(reinterpret_cast<const s16x4*>(row) + (lane & 1)));
             const s16x4 hi =
                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row + 16 * NC) + (lane & 1)));
             return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -595,7 +596,8 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         if (r >= rows) continue;
         if (whole) {
           const int node = by_group.div(r), head = g * group + r - node * group;
-          T* out = static_cast<T*>(x->a.out) + b * x->a.out_stride[0] + node * x->a.out_stride[1] + head * x->a.out_stride[2] + lg * 4;
+          T* out = static_cast<T*>(x->a.out) + b * x->a.out_stride[0] + node * x->a.out_stride[1] +
+                   head * x->a.out_stride[2] + lg * 4;
           const float inv = z[rt] == 0.f ? 0.f : 1.f / z[rt];
 #pragma unroll
           for (int dt = 0; dt < ND; ++dt)
@@ -675,7 +677,8 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(AttnArgs args,
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int i = i0 + k * kSlices + slice;
-        const float wi = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((i < here ? i : 0) * 4, __builtin_bit_cast(int, w)));
+        const float wi = __builtin_bit_cast(
+            float, __builtin_amdgcn_ds_bpermute((i < here ? i : 0) * 4, __builtin_bit_cast(int, w)));
         if (i < here) o += v[k] * wi;
       }
     }
@@ -776,8 +779,8 @@ void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t
   const int rows = a.kv_heads * p.rows, tile_rows = 16 * RT * RG;
   const FastDiv by_tile = fast_div(tile_rows);
   if ((int64_t)rows * a.batch < kCUs * 4)  // too few rows to fill the chip with a wave each
-    hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4, 4>), dim3(rows, a.batch), dim3(256), 0, stream, AttnArgs{a, p}, by_tile,
-                       tile_rows);
+    hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4, 4>), dim3(rows, a.batch), dim3(256), 0, stream,
+                       AttnArgs{a, p}, by_tile, tile_rows);
   else
     hipLaunchKernelGGL((tree_attention_join_kernel<DT, DP / 4, 1>), dim3((rows + 3) / 4, a.batch), dim3(256), 0, stream,
                        AttnArgs{a, p}, by_tile, tile_rows);
