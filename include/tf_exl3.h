@@ -307,8 +307,9 @@ int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int 
  * all of them, and the tree's node t (k[b][t], v[b][t]) where bit t of mask[b][i]
  * is set. A node that sees no key gets zeros. Products of the 16-bit inputs are
  * summed in fp32; probabilities are rounded to the inputs' type for the second
- * product (half an ulp each, unbiased), their sum and the output stay in fp32
- * until the one rounding of the output. A value that no node may see never
+ * product: half an ulp each, and in fp16, for one below 2^-27 of the row's largest, up to
+ * 2^-38 of that largest. Their sum and the output stay in fp32 until the one rounding of
+ * the output. A value that no node may see never
  * reaches an output, infinities and NaN included.
  *
  * Position p of sequence b is slot p % page_size of page table[b][p / page_size].

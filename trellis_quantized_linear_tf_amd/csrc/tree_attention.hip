@@ -13,7 +13,8 @@
 // step taken in the order {4g .. 4g+3, 16+4g .. 16+4g+3} for lane group g, in which V^T is
 // read from shared memory by the transposing loads. Scores, statistics and outputs are
 // in fp32; probabilities are rounded to the inputs' type for the second product (half a
-// unit in the last place each, which the sum of fp32 probabilities does not see).
+// unit in the last place each, which the sum of fp32 probabilities does not see; `Weights` below
+// says how far down fp16 holds that).
 //
 // All tiles of all sequences, heads and row tiles stand in one line, which the workgroups,
 // as many as the chip holds at a time, cut into pieces of equal time, whatever the lengths are:
@@ -56,7 +57,7 @@ struct AttnPlan {
   int groups;          // kv_heads * row_tiles, each with all tiles of a sequence
   int workgroups;      // pieces, at most; 0: one for each group of each sequence
   int min_piece;       // tiles
-  float c, slack;      // |scale| log2(e); 8 / c
+  float c, slack;      // |scale| log2(e); the type's slack in scores
   bool negate;         // scale < 0
   uint32_t page_bytes, slot_bytes;  // of both caches, where they are the same and below 4 GiB
   int step_cols, step_slots;        // a tile in pages and slots
@@ -131,6 +132,16 @@ __device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {
   if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
   return n / d;
 }
+
+// A row's weights for the second product are 2^(x - base + kUp), its base at most kSlack below its
+// largest score so far. bf16 has fp32's exponents. fp16 begins at 2^-14 and ends at 2^16: a base that stands
+// for 2^13 keeps half a unit in the last place down to 2^-27 of the row's largest weight, and 2^-38 of that below
+// (half a step of the subnormals). Slacks of 2^8, 2^4, 2^3, 2^2 and 1 with the room used up, fp16, us: 64-node trees
+// 65.7 / 65.5 / 66.0 / 67.4 / 71.9, 32 x 16 nodes over 16384 positions 394 to 396 for all.
+template <int DT>
+struct Weights {
+  static constexpr float kUp = DT == TF_DT_F16 ? 13.f : 0.f, kSlack = DT == TF_DT_F16 ? 2.f : 8.f;
+};
 
 // A value that all lanes have, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -466,10 +477,9 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
           }
 
           // The base m of a row's exponents is raised, and its sums scaled, only where a score has
-          // grown past it by a factor of 2^8: probabilities up to that lose nothing in any type here.
-          // Until then a lane looks at its own positions alone.
+          // grown past it by the type's slack. Until then a lane looks at its own positions alone. (One look
+          // for all row tiles cost 69.2 us against 67.4 in fp16's 64-node trees.)
           float top[RT];
-          bool grow = false;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             top[rt] = s[0][rt][0];
@@ -477,23 +487,21 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
             for (int t = 0; t < NK; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], s[t][rt][i]);
-            grow = grow || top[rt] > m[rt] + slack;
           }
-          if (__ballot(grow)) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              const float up = fmaxf(m[rt], groups_max(top[rt]));
-              const float keep = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - up) * scale_c);
-              m[rt] = up;
-              z[rt] *= keep;
+          for (int rt = 0; rt < RT; ++rt) {
+            if (!__ballot(top[rt] > m[rt] + slack)) continue;
+            const float up = fmaxf(m[rt], groups_max(top[rt]));
+            const float keep = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - up) * scale_c);
+            m[rt] = up;
+            z[rt] *= keep;
 #pragma unroll
-              for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
-            }
+            for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
           }
           u32x4 pf[NB][RT];
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const float mc = m[rt] == -INFINITY ? 0.f : m[rt] * scale_c;
+            const float mc = (m[rt] == -INFINITY ? 0.f : m[rt] * scale_c) - Weights<DT>::kUp;
             float sum = 0.f;
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
@@ -828,7 +836,8 @@ hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream
   // A scale of 0 keeps masked scores apart from others: the smallest factor does the same to sums.
   const float c = fabsf(a.scale) * 1.4426950408889634f;
   l.p.c = c > 1.2e-38f ? c : 1.2e-38f;
-  l.p.slack = fminf(8.f / l.p.c, 3e38f);
+  const float slack = a.dtype == TF_DT_F16 ? Weights<TF_DT_F16>::kSlack : Weights<TF_DT_BF16>::kSlack;
+  l.p.slack = fminf(slack / l.p.c, 3e38f);
   l.p.negate = a.scale < 0.f;
   const int64_t page = a.k_cache_stride[0] * 2, slot = a.k_cache_stride[1] * 2;
   const bool same = a.v_cache_stride[0] * 2 == page && a.v_cache_stride[1] * 2 == slot;
