@@ -54,3 +54,33 @@ def test_what_stands_beside_one_dominant_key(gpu, dt, dim, nodes, hq, gap):
         over = np.abs(got - want) - tol
         worst = np.unravel_index(over.argmax(), over.shape)
         assert over.max() <= 0, f"key {at}: {got[worst]:.6g} for {want[worst]:.6g}, {over.max():.3g} over the bound"
+
+
+@pytest.mark.parametrize("dt,size", [("f16", 2.0 ** 4), ("f16", 2.0 ** 14), ("f16", 2.0 ** 15), ("bf16", 2.0 ** 15),
+                                     ("bf16", 2.0 ** 30), ("bf16", 2.0 ** 100)])
+@pytest.mark.parametrize("scale", [1.0, -0.3, 0.0078125])
+@pytest.mark.parametrize("dim,nodes,hq", [(64, 1, 2), (128, 9, 12), (128, 40, 12), (256, 24, 8)])
+def test_scores_beyond_what_fp32_resolves(gpu, dt, size, scale, dim, nodes, hq):
+    """Scores are exact products, a few units of `size` apart at up to 20000 of them and more than 1000
+    apart after the scale: the largest alone has weight (or two that are equal, half each)."""
+    say(f"far scores {dt} {size} {scale} {dim} {nodes}")
+    case = Case(dim, dt, [900, 257], nodes, hq, 2, dim, 64, masks=[[0] * nodes] * 2)
+    case.scale = scale
+    case.q[:] = 0
+    case.q[..., 0] = size * (2048 if dt == "f16" and size < 2 ** 10 else 1)
+    g = torch.Generator().manual_seed(dim)
+    unit = 32.0 if dt == "f16" else 128.0
+    for b, n in enumerate(case.lengths):
+        rank = torch.randperm(int(n), generator=g) % (100 if b else 200)  # sequence 0 has every rank more than once
+        if b:
+            rank[torch.randint(0, int(n), (1,), generator=g)] = 105  # sequence 1 one largest
+        else:
+            top = (rank == rank.max()).nonzero()[:, 0]
+            rank[top[2:]] = 0
+        for p in range(int(n)):
+            case.kc[case.table[b, p // 64], p % 64, :, 0] = (unit * rank[p] + 64 * unit if dt == "f16" else unit * (rank[p] + 1)) * (
+                1 if scale > 0 else -1)
+    got = tq.tree_attention(**case.gpu(), scale=scale).double().cpu().numpy()
+    want, _, _ = case.oracle()
+    h = torch.finfo(DT[dt]).eps / 2
+    assert (np.abs(got - want) <= (h + 2.0 ** -20) * np.abs(want) + 2.0 ** -25).all()

@@ -259,6 +259,7 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
   constexpr int kJoin = KG > 1 ? (KG - 1) * RG * ND * 64 : 0;  // other key groups' outputs, one row tile at a time
   __shared__ u32x4 lds[2 * BUF * kTile > kJoin ? 2 * BUF * kTile : kJoin];
   __shared__ float2 join_stat[KG > 1 ? (KG - 1) * RG * 64 : 1];
+  __shared__ uint64_t row_masks[16 * RT * RG];  // looked at in few tiles; registers are short in the widest form
   __shared__ int odd_values;
 
   ArgPtr x = arguments();
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
     const int row0 = (row_tile * RG + rg) * 16 * RT;
     const bool active = row0 < x->p.rows;
     u32x4 q[RT][NQ];
-    uint64_t seen[RT];
+    const uint64_t* masks = row_masks + rg * 16 * RT + (lane & 15);
     {
       const int rows = x->p.rows, group = x->p.group, dim = x->a.head_dim;
       const FastDiv by_group = copy(&x->p.by_group);
@@ -298,7 +299,8 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         const int r = row0 + rt * 16 + (lane & 15), have = min(r, rows - 1);
         const int node = by_group.div(have), head = g * group + have - node * group;
         const T* row = static_cast<const T*>(x->a.q) + b * x->a.q_stride[0] + node * x->a.q_stride[1] + head * x->a.q_stride[2];
-        seen[rt] = r < rows ? (uint64_t)x->a.mask[(int64_t)b * nodes + node] : 0;
+        if (kg == 0 && lg == 0)
+          row_masks[rg * 16 * RT + rt * 16 + lane] = r < rows ? (uint64_t)x->a.mask[(int64_t)b * nodes + node] : 0;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           const int d = i * 32 + lg * 8;
@@ -444,11 +446,14 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         __syncthreads();  // the tile is there, and with BUF 2 the one before it no longer in use
         if (active) {
           const u32x4* tile = lds + half;
+          // Scores relative to the row's base m, which the products are summed onto: however large scores
+          // are, those that have weight are near 0 here, and no rounding of a scaled base is in their
+          // exponents (it left nothing, or infinities, from 2^23 on in fp16; 64-node trees 65.7 -> 66.1 us).
           f32x4 s[NK][RT];
 #pragma unroll
           for (int t = 0; t < NK; ++t)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) s[t][rt] = f32x4(0.f);
+            for (int rt = 0; rt < RT; ++rt) s[t][rt] = f32x4(m[rt] == -INFINITY ? 0.f : -m[rt]);
           // Operands are read kAhead products ahead, or a product would wait out the read of its own.
           constexpr int kAhead = RT == 3 ? 1 : 2, kRing = kAhead + 1;
           u32x4 kf[kRing];
@@ -465,11 +470,12 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
 
           if (edge) {
 #pragma unroll
-            for (int t = 0; t < NK; ++t) {
-              const int j = at + kg * KW + t * 16 + lg * 4;  // the first of the lane's four
+            for (int rt = 0; rt < RT; ++rt) {
+              const uint64_t seen = masks[rt * 16];
 #pragma unroll
-              for (int rt = 0; rt < RT; ++rt) {
-                const uint32_t bits = seen_of(seen[rt], j - len, stop - j);
+              for (int t = 0; t < NK; ++t) {
+                const int j = at + kg * KW + t * 16 + lg * 4;  // the first of the lane's four
+                const uint32_t bits = seen_of(seen, j - len, stop - j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[t][rt][i] = (bits >> i) & 1 ? s[t][rt][i] : -INFINITY;
               }
@@ -490,25 +496,28 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
           }
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            if (!__ballot(top[rt] > m[rt] + slack)) continue;
-            const float up = fmaxf(m[rt], groups_max(top[rt]));
-            const float keep = m[rt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m[rt] - up) * scale_c);
-            m[rt] = up;
+            const bool none = m[rt] == -INFINITY;
+            if (!__ballot(top[rt] > (none ? -INFINITY : slack))) continue;
+            const float most = groups_max(top[rt]);
+            const float up = none ? (most == -INFINITY ? 0.f : most) : fmaxf(most, 0.f);
+            const float keep = none ? 0.f : __builtin_amdgcn_exp2f(-up * scale_c);
+            m[rt] = none ? most : m[rt] + up;
             z[rt] *= keep;
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
+#pragma unroll
+            for (int t = 0; t < NK; ++t) s[t][rt] -= up;
           }
           u32x4 pf[NB][RT];
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const float mc = (m[rt] == -INFINITY ? 0.f : m[rt] * scale_c) - Weights<DT>::kUp;
             float sum = 0.f;
 #pragma unroll
             for (int t = 0; t < NK; ++t) {
               float e[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], scale_c, -mc));
+                e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], scale_c, Weights<DT>::kUp));
                 sum += e[i];
               }
               pf[t / 2][rt][(t & 1) * 2] = pack2<DT>(e[0], e[1]);
@@ -590,7 +599,7 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
             for (int i = 0; i < 4; ++i) {
               const float v = Elem<DT>::load(row[dt * 16 + lg * 4 + i]), odd = fabsf(v) < INFINITY ? 0.f : v;
 #pragma unroll
-              for (int rt = 0; rt < RT; ++rt) o[dt][rt][i] += (seen[rt] >> (j - len)) & 1 ? odd : 0.f;
+              for (int rt = 0; rt < RT; ++rt) o[dt][rt][i] += (masks[rt * 16] >> (j - len)) & 1 ? odd : 0.f;
             }
           }
         }
