@@ -35,24 +35,27 @@ struct ChainEnd {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// 2^y for y <= 0 in 64 bits: 2^n 2^f with f = y - n in [-1/2, 1/2] and 2^f by the polynomial of
-// degree 9 that equals it at the ten Chebyshev nodes of that range: 1.9e-14 relative, which
-// over a row of 129280 moves the running sum past a random number with a chance of 1e-9.
+// 2^y for y <= 0 in 64 bits: 2^n 2^f with f = y - n in [-1/2, 1/2] and 2^f = 1 + f g(f), g the
+// polynomial of degree 9 that equals (2^f - 1) / f at the ten Chebyshev nodes of that range: 5.7e-16
+// relative at most, to both sides alike, and exact at 0.
 __device__ __forceinline__ double pow2_poly(double f) {
-  double p = 0x1.b6571de2f2351p-24;
-  p = __builtin_fma(p, f, 0x1.63ef969a64d3cp-20);
+  double p = 0x1.e5e9f548e5725p-28;
+  p = __builtin_fma(p, f, 0x1.b6571de2f2351p-24);
+  p = __builtin_fma(p, f, 0x1.62bfe46117445p-20);
   p = __builtin_fma(p, f, 0x1.ffcb76789860fp-17);
-  p = __builtin_fma(p, f, 0x1.43088e257f341p-13);
+  p = __builtin_fma(p, f, 0x1.4309130378460p-13);
   p = __builtin_fma(p, f, 0x1.5d87fe908f88ap-10);
-  p = __builtin_fma(p, f, 0x1.3b2ab72b175eep-7);
+  p = __builtin_fma(p, f, 0x1.3b2ab6fba385fp-7);
   p = __builtin_fma(p, f, 0x1.c6b08d7044119p-5);
-  p = __builtin_fma(p, f, 0x1.ebfbdff8149f2p-3);
+  p = __builtin_fma(p, f, 0x1.ebfbdff82c590p-3);
   p = __builtin_fma(p, f, 0x1.62e42fefa39f7p-1);
   return __builtin_fma(p, f, 1.0);
 }
 
 // For sums, 64 table entries 2^(j / 64), j = 0 .. 63, in shared memory shorten that: with y = (64 n + j
-// + r) / 64, 2^y = 2^n 2^(j / 64) 2^(r / 64), the last by a polynomial of degree 4 (2.4e-15 relative).
+// + r) / 64, 2^y = 2^n 2^(j / 64) 2^(r / 64), the last by a polynomial of degree 4 (2.4e-15 relative at
+// most, to both sides alike). A running sum is off by less than 3e-15 of the row's sum and the sums' own
+// roundings, which over a row of 129280 moves it past a random number with a chance of 1e-9 at most.
 // What is below 2^-1000 (-inf and NaN too) counts as that, which no sum with a 1 in it can tell
 // from 0. Adding 1.5 2^52 rounds 64 y to an integer in the low word; shifted by 14 bits it adds n to the
 // exponent, and j 2^14 which the entries have been lowered by.
