@@ -19,7 +19,8 @@
  *  - Data pointers are DEVICE pointers owned by the caller. The library
  *    allocates nothing, frees nothing and keeps no mutable global state; calls
  *    are thread-safe.
- *  - `stream` is a hipStream_t (NULL = the default stream). Launches are
+ *  - `stream` is a hipStream_t (NULL = the default stream of the calling thread's current
+ *    device), which the pointers' device has to be. Launches are
  *    asynchronous; the caller synchronizes.
  *  - Arguments are checked on the host before anything is launched. On a
  *    refusal (negative status) nothing is launched and nothing is written.

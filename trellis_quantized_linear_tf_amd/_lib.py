@@ -272,6 +272,18 @@ def _stream(t) -> int:
     return _raw_stream(t.get_device())
 
 
+def _run(t, fn, *args) -> None:
+    """fn(*args, stream) on the tensor's GPU, made current where another is: a default stream's handle
+    is 0 on every GPU and means the current one's."""
+    cuda = _torch().cuda
+    device = t.get_device()
+    if device == cuda.current_device():
+        _check(fn(*args, _stream(t)))
+        return
+    with cuda.device(device):
+        _check(fn(*args, _stream(t)))
+
+
 def rot_in(x, suh, z=None):
     """z[rows][in_dim] fp16 = rot_in(x, suh); x is fp32/fp16/bf16 [rows][in_dim], suh fp16 [in_dim]."""
     torch = _torch()
@@ -283,7 +295,7 @@ def rot_in(x, suh, z=None):
     _same_gpu(x, suh, z)
     if z is None:
         z = torch.empty((rows, in_dim), dtype=torch.float16, device=x.device)
-    _check(load().tf_exl3_rot_in(_ptr(x), _dt_code(x.dtype), _ptr(suh), _ptr(z), rows, in_dim, _stream(x)))
+    _run(x, load().tf_exl3_rot_in, _ptr(x), _dt_code(x.dtype), _ptr(suh), _ptr(z), rows, in_dim)
     return z
 
 
@@ -319,8 +331,7 @@ def linear(z, trellis, svh, bits: int, out_dim: int, y=None, out_dtype=None, wav
     lib = load()
     fn = {"dot2": lib.tf_exl3_linear, "mfma": lib.tf_exl3_linear_mfma, "prompt": lib.tf_exl3_linear_prompt,
           "strips": lib.tf_exl3_linear_strips}[engine]
-    _check(fn(bits, rows, in_dim, out_dim, _ptr(z), _ptr(trellis), _ptr(svh), _ptr(y), _dt_code(y.dtype), waves,
-              _stream(z)))
+    _run(z, fn, bits, rows, in_dim, out_dim, _ptr(z), _ptr(trellis), _ptr(svh), _ptr(y), _dt_code(y.dtype), waves)
     return y
 
 
@@ -334,7 +345,7 @@ def repack_strips(trellis, bits: int, in_dim: int, out_dim: int, out=None):
     _same_gpu(trellis, out)
     if out is None:
         out = torch.empty_like(trellis)
-    _check(load().tf_exl3_repack_strips(bits, in_dim, out_dim, _ptr(trellis), _ptr(out), _stream(trellis)))
+    _run(trellis, load().tf_exl3_repack_strips, bits, in_dim, out_dim, _ptr(trellis), _ptr(out))
     return out
 
 
@@ -353,8 +364,8 @@ def project(x, suh, trellis, svh, bits: int, out_dim: int, y=None, out_dtype=Non
     _same_gpu(x, suh, trellis, svh, y)
     if y is None:
         y = torch.empty((rows, out_dim), dtype=out_dtype or torch.float32, device=x.device)
-    _check(load().tf_exl3_project(bits, rows, in_dim, out_dim, _ptr(x), _dt_code(x.dtype), _ptr(suh),
-                                  _ptr(trellis), _ptr(svh), _ptr(y), _dt_code(y.dtype), waves, _stream(x)))
+    _run(x, load().tf_exl3_project, bits, rows, in_dim, out_dim, _ptr(x), _dt_code(x.dtype), _ptr(suh),
+         _ptr(trellis), _ptr(svh), _ptr(y), _dt_code(y.dtype), waves)
     return y
 
 
@@ -370,7 +381,7 @@ def debug_decode_states(states):
     _same_gpu(states)
     s = states.to(torch.int16) if states.dtype != torch.int16 else states
     w = torch.empty_like(s)
-    _check(load().tf_exl3_debug_decode_states(_ptr(s), _ptr(w), s.numel(), _stream(s)))
+    _run(s, load().tf_exl3_debug_decode_states, _ptr(s), _ptr(w), s.numel())
     return w
 
 
@@ -380,7 +391,7 @@ def debug_decode_tiles(trellis, bits: int, in_dim: int, out_dim: int):
     _need("trellis", trellis, nbytes=_stream_bytes(bits, in_dim, out_dim))
     _same_gpu(trellis)
     w = torch.empty((in_dim, out_dim), dtype=torch.float16, device=trellis.device)
-    _check(load().tf_exl3_debug_decode_tiles(bits, in_dim, out_dim, _ptr(trellis), _ptr(w), _stream(trellis)))
+    _run(trellis, load().tf_exl3_debug_decode_tiles, bits, in_dim, out_dim, _ptr(trellis), _ptr(w))
     return w
 
 
@@ -392,8 +403,8 @@ def debug_linear_split(z, trellis, svh, bits: int, out_dim: int, split: int, y=N
     rows, in_dim = _check_linear_args(z, trellis, svh, bits, out_dim, y, out_dtype)
     if y is None:
         y = torch.empty((rows, out_dim), dtype=out_dtype or torch.float32, device=z.device)
-    _check(load().tf_exl3_debug_linear_split(bits, rows, in_dim, out_dim, _ptr(z), _ptr(trellis), _ptr(svh), _ptr(y),
-                                             _dt_code(y.dtype), waves, split, _stream(z)))
+    _run(z, load().tf_exl3_debug_linear_split, bits, rows, in_dim, out_dim, _ptr(z), _ptr(trellis), _ptr(svh), _ptr(y),
+         _dt_code(y.dtype), waves, split)
     return y
 
 
@@ -405,8 +416,8 @@ def debug_linear_mfma_split(z, trellis, svh, bits: int, out_dim: int, split: int
     rows, in_dim = _check_linear_args(z, trellis, svh, bits, out_dim, y, out_dtype)
     if y is None:
         y = torch.empty((rows, out_dim), dtype=out_dtype or torch.float32, device=z.device)
-    _check(load().tf_exl3_debug_linear_mfma_split(bits, rows, in_dim, out_dim, _ptr(z), _ptr(trellis), _ptr(svh),
-                                                  _ptr(y), _dt_code(y.dtype), waves, split, _stream(z)))
+    _run(z, load().tf_exl3_debug_linear_mfma_split, bits, rows, in_dim, out_dim, _ptr(z), _ptr(trellis), _ptr(svh),
+         _ptr(y), _dt_code(y.dtype), waves, split)
     return y
 
 
@@ -415,7 +426,7 @@ def calib_copy(src, dst, blocks: int = 2048):
     nbytes = _nbytes(src)
     _need("dst", dst, nbytes=nbytes)
     _same_gpu(src, dst)
-    _check(load().tf_exl3_calib_copy(_ptr(src), _ptr(dst), nbytes, blocks, _stream(src)))
+    _run(src, load().tf_exl3_calib_copy, _ptr(src), _ptr(dst), nbytes, blocks)
 
 
 def calib_stream_read(src, out):
@@ -427,4 +438,4 @@ def calib_stream_read(src, out):
         raise ValueError("out must hold a positive multiple of 256 int32 words (one per thread)")
     blocks = out.numel() // 256
     _same_gpu(src, out)
-    _check(load().tf_exl3_calib_stream_read(_ptr(src), nbytes, _ptr(out), blocks, _stream(src)))
+    _run(src, load().tf_exl3_calib_stream_read, _ptr(src), nbytes, _ptr(out), blocks)

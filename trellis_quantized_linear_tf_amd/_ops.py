@@ -13,7 +13,7 @@ from __future__ import annotations
 import struct
 
 from . import _lib
-from ._lib import _check, _dt_code, _stream, _torch, load
+from ._lib import _dt_code, _run, _torch, load
 
 
 def _need(name, t, dim, dtypes, shape=None):
@@ -154,7 +154,7 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
         q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), need, *sq[:3], *sk[:3], *sv[:3],
         *skc[:3], *svc[:3], *out.stride()[:3], table.stride(0))
-    _check(lib.tf_exl3_tree_attention(a, _stream(q)))
+    _run(q, lib.tf_exl3_tree_attention, a)
     return out
 
 
@@ -213,7 +213,7 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None
         a, 0, k.element_size(), batch, tokens, heads, dim, pages[0], pages[1], columns, k.data_ptr(), v.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), _ptr(nodes) or 0, _ptr(counts) or 0,
         *sk[:3], *sv[:3], *skc[:3], *svc[:3], table.stride(0))
-    _check(load().tf_exl3_cache_append(a, _stream(k)))
+    _run(k, load().tf_exl3_cache_append, a)
 
 
 def _check_drafts(logits, tokens, u, temperature):
@@ -270,10 +270,10 @@ def verify_tree(logits, tokens, parents, u, temperature=None):
     lib = load()
     need = lib.tf_exl3_verify_workspace(batch, nodes, vocab)
     ws = _workspace(need, logits)
-    _check(lib.tf_exl3_verify_tree(
+    _run(logits, lib.tf_exl3_verify_tree,
         _dt_code(logits.dtype), batch, nodes, vocab, logits.data_ptr(), logits.stride(0), logits.stride(1),
         tokens.data_ptr(), parents.data_ptr(), u.data_ptr(), _ptr(temperature), accepted.data_ptr(),
-        count.data_ptr(), after.data_ptr(), ws.data_ptr(), ws.numel(), _stream(logits)))
+        count.data_ptr(), after.data_ptr(), ws.data_ptr(), ws.numel())
     return accepted, count, after
 
 
@@ -302,10 +302,10 @@ def verify_chain(logits, tokens, q, u, temperature=None):
     lib = load()
     need = lib.tf_exl3_verify_workspace(batch, nodes, vocab)
     ws = _workspace(need, logits)
-    _check(lib.tf_exl3_verify_chain(
+    _run(logits, lib.tf_exl3_verify_chain,
         _dt_code(logits.dtype), batch, nodes, vocab, logits.data_ptr(), logits.stride(0), logits.stride(1),
         tokens.data_ptr(), _ptr(q) if nodes > 1 else None, q.stride(0), q.stride(1), u.data_ptr(),
-        _ptr(temperature), count.data_ptr(), after.data_ptr(), ws.data_ptr(), ws.numel(), _stream(logits)))
+        _ptr(temperature), count.data_ptr(), after.data_ptr(), ws.data_ptr(), ws.numel())
     return count, after
 
 
@@ -342,10 +342,9 @@ def _distill(logits, index, top, weight, temperature, want_loss, want_grad):
     code = _dt_code(logits.dtype)
     need = lib.tf_exl3_distill_workspace(code, rows, vocab, index.shape[1])
     ws = _workspace(need, logits)
-    _check(lib.tf_exl3_distill(
+    _run(logits, lib.tf_exl3_distill,
         code, rows, vocab, index.shape[1], logits.data_ptr(), logits.stride(0), index.data_ptr(), top.data_ptr(),
-        _dt_code(top.dtype), _ptr(weight), temperature, _ptr(loss), _ptr(grad), vocab, ws.data_ptr(), ws.numel(),
-        _stream(logits)))
+        _dt_code(top.dtype), _ptr(weight), temperature, _ptr(loss), _ptr(grad), vocab, ws.data_ptr(), ws.numel())
     return loss, grad
 
 
