@@ -10,6 +10,7 @@ and what happens to out-of-range values on the device, stand in include/tf_exl3.
 
 from __future__ import annotations
 
+import functools
 import struct
 
 from . import _lib
@@ -70,6 +71,56 @@ def _floats():
     return (torch.float32, torch.float16, torch.bfloat16)
 
 
+def _followed(*tensors) -> bool:
+    """Whether autograd follows a tensor, backward or (a tangent within a dual level) forward."""
+    torch = _torch()
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    forward = torch.autograd.forward_ad
+    return forward._current_level >= 0 and any(
+        t is not None and forward.unpack_dual(t).tangent is not None for t in tensors)
+
+
+@functools.cache
+def _nodes():
+    """The calls' nodes in autograd's graph. None has a forward mode, which autograd itself refuses then."""
+    torch = _torch()
+    from torch.autograd.function import once_differentiable
+
+    class WithoutGradient(torch.autograd.Function):
+        """A result whose inputs it gives no gradient: asking for one is an error, not a zero."""
+
+        @staticmethod
+        def forward(ctx, name, result, *inputs):
+            ctx.name = name
+            return result.detach()
+
+        @staticmethod
+        def backward(ctx, *_):
+            raise RuntimeError(f"{ctx.name} has no gradient: call it under torch.no_grad() or on detached tensors")
+
+    class DistillLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, index, top, weight, temperature, want_grad):
+            ctx.save_for_backward(logits, index, top)
+            ctx.temperature = temperature
+            loss, grad = _distill(logits, index, top, weight, temperature, True, want_grad)
+            if want_grad:
+                ctx.mark_non_differentiable(grad)
+            return loss, grad
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, weight, _):
+            if ctx.needs_input_grad[2]:
+                raise RuntimeError("the distillation loss has no gradient by the teacher's logits: pass top.detach()")
+            logits, index, top = ctx.saved_tensors
+            grad = _distill(logits, index, top, weight.contiguous(), ctx.temperature, False, True)[1]
+            return grad, None, None, None, None, None
+
+    return WithoutGradient, DistillLoss
+
+
 # Every call looks its arguments over with one chain of comparisons, which implies all of
 # the checks below and costs a few microseconds; only a call that does not pass it goes
 # through them one by one, for the message (or because a dimension of 1 has an odd stride).
@@ -112,7 +163,10 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
     bit t of a node's mask says that it sees node t (1..64 nodes). k_cache, v_cache [pages]
     [page_size][kv_heads][dim], in any order of memory with contiguous rows; table int32
     [batch][table_pages]; lengths int32 [batch]: positions in the cache, all of them seen.
-    scale defaults to dim ** -0.5. A node that sees nothing gets zeros."""
+    scale defaults to dim ** -0.5. A node that sees nothing gets zeros.
+
+    It has no gradient: where autograd follows an input, the result (not `out` itself) is part of
+    its graph, and a backward pass that reaches it raises."""
     torch = _torch()
     dev = -1
     try:
@@ -155,6 +209,8 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
         table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), need, *sq[:3], *sk[:3], *sv[:3],
         *skc[:3], *svc[:3], *out.stride()[:3], table.stride(0))
     _run(q, lib.tf_exl3_tree_attention, a)
+    if _followed(q, k, v, k_cache, v_cache):
+        return _nodes()[0].apply("tree_attention", out, q, k, v, k_cache, v_cache)
     return out
 
 
@@ -179,7 +235,8 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None
     """Writes rows of k and v [batch][tokens][kv_heads][dim] behind the lengths[b] positions
     that a sequence has in the cache (tf_exl3_cache_append). nodes int32 [batch][tokens] and
     counts int32 [batch] choose them: position lengths[b] + j takes row nodes[b][j], for
-    j < counts[b] (verify_tree's `accepted` and `count` fit). lengths stays as it is."""
+    j < counts[b] (verify_tree's `accepted` and `count` fit). lengths stays as it is. The cache
+    takes values: to autograd its rows are constants."""
     torch = _torch()
     dev = -1
     try:
@@ -351,15 +408,21 @@ def _distill(logits, index, top, weight, temperature, want_loss, want_grad):
 def distill_loss(logits, index, top, temperature=1.0):
     """loss fp32 [rows] of logits [rows][vocab] against a teacher's top logits: top [rows]
     [top_k] at the places index int32 [rows][top_k], entries with an index outside the
-    vocabulary (-1) left out (tf_exl3_distill)."""
+    vocabulary (-1) left out (tf_exl3_distill). Under autograd its backward pass is distill_grad;
+    there is none by the teacher's logits, and no second one."""
+    if _followed(logits, top):
+        return _nodes()[1].apply(logits, index, top, None, temperature, False)[0]
     return _distill(logits, index, top, None, temperature, True, False)[0]
 
 
 def distill_grad(logits, index, top, weight, temperature=1.0):
-    """The gradient of sum(weight * loss) by logits, of the logits' type; weight fp32 [rows]."""
+    """The gradient of sum(weight * loss) by logits, of the logits' type; weight fp32 [rows]. To
+    autograd it is a constant."""
     return _distill(logits, index, top, weight, temperature, False, True)[1]
 
 
 def distill(logits, index, top, weight, temperature=1.0):
-    """(loss, grad) in one call: distill_loss and distill_grad."""
+    """(loss, grad) in one call: distill_loss, which autograd may follow, and distill_grad."""
+    if _followed(logits, top):
+        return _nodes()[1].apply(logits, index, top, weight, temperature, True)
     return _distill(logits, index, top, weight, temperature, True, True)
