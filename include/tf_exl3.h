@@ -292,7 +292,8 @@ int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int 
  * Strides are in elements. Innermost dimensions are contiguous (stride 1); a stride
  * over a dimension of 1 is not looked at. What lives on the device (lengths, page numbers, masks, node numbers, parents,
  * tokens) cannot be refused on the host: every kernel bounds it before an
- * address is made of it, as stated at each call. A workspace belongs to one call
+ * address is made of it, as stated at each call. Sizes whose launches would have 2^32
+ * work-items or more are refused (TF_E_SIZE) before the first launch. A workspace belongs to one call
  * at a time, needs no initial contents and may be used again, or freed in
  * stream order, after the call.
  */
@@ -408,7 +409,8 @@ int tf_exl3_cache_append(const tf_exl3_cache_append_args* a, void* stream);
  *
  *   q fp32 [batch][nodes - 1][vocab], strides of batch and node
  *
- * Limits: nodes 1 .. 1024, vocab below 2^31. workspace: the call's *_workspace bytes,
+ * Limits: nodes 1 .. 1024, vocab below 2^31, batch * nodes * ceil(vocab / 2048) at most
+ * 2^26 - 4, for a tree batch * nodes below 2^24. workspace: the call's *_workspace bytes,
  * 16-byte aligned.
  */
 int tf_exl3_verify_tree(int dtype, int batch, int nodes, int vocab, const void* logits, int64_t stride_batch,
@@ -436,7 +438,8 @@ size_t tf_exl3_verify_workspace(int batch, int nodes, int vocab);
  * maxima and the logarithm are in fp32.
  *
  *   loss     fp32 [rows] or NULL;  grad [rows][vocab] of the logits' type or NULL
- *   logits   [rows][vocab], rows logits_stride apart; rows may begin at any element
+ *   logits   [rows][vocab], rows logits_stride apart; rows may begin at any element; rows below
+ *            2^24, 2^23 where one has more than 32 KiB, 2^22 where it has more than 128 KiB
  *   index    int32 [rows][top_k], top of type top_dtype [rows][top_k], top_k 1 .. 1024
  *   weight   fp32 [rows] (needed for grad)
  *   workspace tf_exl3_distill_workspace bytes, 16-byte aligned

@@ -107,7 +107,7 @@ static bool in_units(const tf_exl3_cache_append_args& a, int bytes) {
 }
 
 template <int BYTES>
-static void launch(const tf_exl3_cache_append_args& a, hipStream_t stream) {
+static AppendPlan plan_of(const tf_exl3_cache_append_args& a) {
   AppendPlan p;
   p.row_units = a.head_dim * a.elem_bytes / BYTES;
   p.units = 2 * a.kv_heads * p.row_units;
@@ -120,19 +120,40 @@ static void launch(const tf_exl3_cache_append_args& a, hipStream_t stream) {
   p.tokens = share < 1 ? 1 : share < most ? (int)share : most;
   p.by_units = fast_div(p.units), p.by_row = fast_div(p.row_units);
   p.by_heads = fast_div(a.kv_heads), p.by_page = fast_div(a.page_size);
-  hipLaunchKernelGGL(cache_append_kernel<BYTES>, dim3((a.tokens + p.tokens - 1) / p.tokens, a.batch), dim3(kAppendThreads), 0,
+  return p;
+}
+
+static int unit_of(const tf_exl3_cache_append_args& a) { return in_units(a, 16) ? 16 : in_units(a, 4) ? 4 : in_units(a, 2) ? 2 : 1; }
+
+static AppendPlan plan_of(const tf_exl3_cache_append_args& a, int unit) {
+  return unit == 16 ? plan_of<16>(a) : unit == 4 ? plan_of<4>(a) : unit == 2 ? plan_of<2>(a) : plan_of<1>(a);
+}
+
+static int64_t workgroups_of(const tf_exl3_cache_append_args& a, const AppendPlan& p) {
+  return ((int64_t)a.tokens + p.tokens - 1) / p.tokens;
+}
+
+template <int BYTES>
+static void launch(const tf_exl3_cache_append_args& a, const AppendPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL(cache_append_kernel<BYTES>, dim3((unsigned)workgroups_of(a, p), a.batch), dim3(kAppendThreads), 0,
                      stream, a, p);
 }
 
+bool cache_append_fits(const tf_exl3_cache_append_args& a) {
+  return launchable(workgroups_of(a, plan_of(a, unit_of(a))), kAppendThreads);
+}
+
 hipError_t launch_cache_append(const tf_exl3_cache_append_args& a, hipStream_t stream) {
-  if (in_units(a, 16))
-    launch<16>(a, stream);
-  else if (in_units(a, 4))
-    launch<4>(a, stream);
-  else if (in_units(a, 2))
-    launch<2>(a, stream);
+  const int unit = unit_of(a);
+  const AppendPlan p = plan_of(a, unit);
+  if (unit == 16)
+    launch<16>(a, p, stream);
+  else if (unit == 4)
+    launch<4>(a, p, stream);
+  else if (unit == 2)
+    launch<2>(a, p, stream);
   else
-    launch<1>(a, stream);
+    launch<1>(a, p, stream);
   return hipGetLastError();
 }
 

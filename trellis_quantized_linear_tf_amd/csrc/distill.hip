@@ -390,6 +390,16 @@ static bool cut(int dtype, int rows, int vocab) {
   return bytes / 16 > kLongRow && (rows <= kFewRows || rows * bytes <= kFewBytes);
 }
 
+// Threads that hold a row between them.
+static int row_threads(int dtype, int vocab) {
+  const int pieces = vocab / (dtype == TF_DT_F32 ? 4 : 8);
+  return pieces <= 256 * 8 ? 256 : pieces <= kLongRow ? 512 : 1024;
+}
+
+bool distill_fits(int dtype, int rows, int vocab) {
+  return cut(dtype, rows, vocab) || launchable(rows, row_threads(dtype, vocab));
+}
+
 template <int DT>
 static void launch(const DistillArgs& a, hipStream_t stream) {
   const int parts = parts_of(DT, a.vocab);
@@ -398,11 +408,11 @@ static void launch(const DistillArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(distill_join_kernel<DT>, dim3(a.grad ? parts : 1, a.rows), dim3(kPartThreads), 0, stream, a, parts);
     return;
   }
-  const int pieces = a.vocab / Elem<DT>::kPiece;
+  const int threads = row_threads(DT, a.vocab);
   const dim3 grid(a.rows);
-  if (pieces <= 256 * 8)
+  if (threads == 256)
     hipLaunchKernelGGL((distill_row_kernel<DT, 256, 8>), grid, dim3(256), 0, stream, a);
-  else if (pieces <= kLongRow)
+  else if (threads == 512)
     hipLaunchKernelGGL((distill_row_kernel<DT, 512, 16>), grid, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((distill_row_kernel<DT, 1024, 16>), grid, dim3(1024), 0, stream, a);

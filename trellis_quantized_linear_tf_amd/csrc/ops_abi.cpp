@@ -62,12 +62,13 @@ int attention_sizes(const tf_exl3_tree_attention_args* a) {
   if (a->batch < 0 || a->batch > kMaxBatch || a->nodes < 1 || a->nodes > kMaxTreeNodes) return TF_E_SIZE;
   if (a->kv_heads < 1 || a->q_heads < 1 || a->q_heads > kMaxBatch || a->q_heads % a->kv_heads != 0) return TF_E_SIZE;
   if (a->head_dim < 16 || a->head_dim > 256 || a->head_dim % 16 != 0) return TF_E_SIZE;
-  return cache_sizes(1, a->page_size, a->table_pages, 0);
+  const int st = cache_sizes(1, a->page_size, a->table_pages, 0);
+  return st != TF_OK || tf_exl3::tree_attention_fits(*a) ? st : TF_E_SIZE;
 }
 
-int verify_sizes(int batch, int nodes, int vocab) {
+int verify_sizes(int batch, int nodes, int vocab, bool tree) {
   if (batch < 0 || batch > kMaxBatch || nodes < 1 || nodes > kMaxVerifyNodes || vocab < 1) return TF_E_SIZE;
-  return TF_OK;
+  return tf_exl3::verify_fits(batch, nodes, vocab, tree) ? TF_OK : TF_E_SIZE;
 }
 
 bool row_strides_ok(int64_t batch, int64_t node) {
@@ -151,6 +152,7 @@ int tf_exl3_cache_append(const tf_exl3_cache_append_args* args, void* stream) {
       !strides_ok(a->v_cache_stride, 1) || !apart(a->pages, a->page_size, a->kv_heads, a->k_cache_stride) ||
       !apart(a->pages, a->page_size, a->kv_heads, a->v_cache_stride))
     return TF_E_SIZE;
+  if (!tf_exl3::cache_append_fits(*a)) return TF_E_SIZE;
   if (a->batch == 0 || a->tokens == 0 || a->table_pages == 0) return TF_OK;
   if (!a->k || !a->v || !a->k_cache || !a->v_cache || !a->table || !a->lengths) return TF_E_NULL;
   const uintptr_t e = (uintptr_t)a->elem_bytes;
@@ -175,7 +177,7 @@ int tf_exl3_cache_append(const tf_exl3_cache_append_args* args, void* stream) {
 }
 
 size_t tf_exl3_verify_workspace(int batch, int nodes, int vocab) {
-  return verify_sizes(batch, nodes, vocab) == TF_OK ? tf_exl3::verify_workspace(batch, nodes, vocab) : 0;
+  return verify_sizes(batch, nodes, vocab, false) == TF_OK ? tf_exl3::verify_workspace(batch, nodes, vocab) : 0;
 }
 
 int tf_exl3_verify_tree(int dtype, int batch, int nodes, int vocab, const void* logits, int64_t stride_batch,
@@ -183,7 +185,7 @@ int tf_exl3_verify_tree(int dtype, int batch, int nodes, int vocab, const void* 
                         const float* temperature, int32_t* accepted, int32_t* count, int32_t* next,
                         void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dtype)) return TF_E_DTYPE;
-  const int st = verify_sizes(batch, nodes, vocab);
+  const int st = verify_sizes(batch, nodes, vocab, true);
   if (st != TF_OK) return st;
   if (!row_strides_ok(stride_batch, stride_node)) return TF_E_SIZE;
   if (batch == 0) return TF_OK;
@@ -220,7 +222,7 @@ int tf_exl3_verify_chain(int dtype, int batch, int nodes, int vocab, const void*
                          int64_t q_stride_node, const float* u, const float* temperature, int32_t* count,
                          int32_t* next, void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dtype)) return TF_E_DTYPE;
-  const int st = verify_sizes(batch, nodes, vocab);
+  const int st = verify_sizes(batch, nodes, vocab, false);
   if (st != TF_OK) return st;
   if (!row_strides_ok(stride_batch, stride_node) || !row_strides_ok(q_stride_batch, q_stride_node)) return TF_E_SIZE;
   if (batch == 0) return TF_OK;
@@ -253,7 +255,8 @@ int tf_exl3_verify_chain(int dtype, int batch, int nodes, int vocab, const void*
 }
 
 size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k) {
-  if (!dtype_ok(dtype) || rows < 0 || vocab < 1 || top_k < 1 || top_k > kMaxTop) return 0;
+  if (!dtype_ok(dtype) || rows < 0 || vocab < 1 || top_k < 1 || top_k > kMaxTop || !tf_exl3::distill_fits(dtype, rows, vocab))
+    return 0;
   return tf_exl3::distill_workspace(dtype, rows, vocab, top_k);
 }
 
@@ -262,7 +265,7 @@ int tf_exl3_distill(int dtype, int rows, int vocab, int top_k, const void* logit
                     float* loss, void* grad, int64_t grad_stride, void* workspace, size_t workspace_bytes,
                     void* stream) {
   if (!dtype_ok(dtype) || !dtype_ok(top_dtype)) return TF_E_DTYPE;
-  if (rows < 0 || vocab < 1 || top_k < 1 || top_k > kMaxTop) return TF_E_SIZE;
+  if (rows < 0 || vocab < 1 || top_k < 1 || top_k > kMaxTop || !tf_exl3::distill_fits(dtype, rows, vocab)) return TF_E_SIZE;
   if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature)) return TF_E_SIZE;
   if (logits_stride < 0 || logits_stride > kMaxStride) return TF_E_SIZE;
   if (grad && (grad_stride < 0 || grad_stride > kMaxStride || (rows > 1 && grad_stride < vocab))) return TF_E_SIZE;

@@ -10,9 +10,15 @@
 
 namespace tf_exl3 {
 
+// The runtime refuses a launch with 2^32 work-items or more in a dimension. Each operator says
+// beforehand whether all launches of a call stay below, so that none is left out behind others.
+inline bool launchable(int64_t workgroups, int threads) { return workgroups * threads < (1ll << 32); }
+
+bool tree_attention_fits(const tf_exl3_tree_attention_args& a);
 hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream);
 size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a);
 
+bool cache_append_fits(const tf_exl3_cache_append_args& a);
 hipError_t launch_cache_append(const tf_exl3_cache_append_args& a, hipStream_t stream);
 
 struct VerifyArgs {
@@ -29,6 +35,7 @@ struct VerifyArgs {
   void* workspace;
 };
 
+bool verify_fits(int batch, int nodes, int vocab, bool tree);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t stream);
 size_t verify_workspace(int batch, int nodes, int vocab);
 
@@ -48,6 +55,7 @@ struct DistillArgs {
   void* workspace;
 };
 
+bool distill_fits(int dtype, int rows, int vocab);
 hipError_t launch_distill(const DistillArgs& a, hipStream_t stream);
 size_t distill_workspace(int dtype, int rows, int vocab, int top_k);
 

@@ -835,9 +835,15 @@ size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a) {
   return l.seq_bytes + l.stat_bytes + l.part_bytes + 16;
 }
 
+// The second launch has a workgroup for no more than each of 64 * 65535 rows, the first with pieces no more
+// of them than the chip holds.
+bool tree_attention_fits(const tf_exl3_tree_attention_args& a) {
+  const Layout l = layout_of(a);
+  return launchable((int64_t)a.batch * l.p.groups, l.s.rg * l.s.kg * 64) || l.p.workgroups > 0;
+}
+
 hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream) {
   Layout l = layout_of(a);
-  if ((int64_t)a.batch * l.p.groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   char* ws = static_cast<char*>(a.workspace);
   l.p.seq = reinterpret_cast<SeqTiles*>(ws);
   l.p.stat = reinterpret_cast<float2*>(ws + l.seq_bytes);

@@ -513,11 +513,16 @@ __global__ __launch_bounds__(kSampleThreads) void chain_next_kernel(VerifyArgs a
 
 static int chunks_of(int vocab) { return (int)(((int64_t)vocab + kChunk - 1) / kChunk); }
 
+// The other launches of a call have fewer work-items than these, whatever its sizes.
+bool verify_fits(int batch, int nodes, int vocab, bool tree) {
+  const int64_t rows = (int64_t)batch * nodes;
+  return launchable((rows * chunks_of(vocab) + kWaves - 1) / kWaves, kWaves * 64) && (!tree || launchable(rows, kSampleThreads));
+}
+
 template <int DT>
 static hipError_t launch(const VerifyArgs& a, hipStream_t stream) {
   const int chunks = chunks_of(a.vocab);
   const int64_t rows = (int64_t)a.batch * a.nodes, groups = (rows * chunks + kWaves - 1) / kWaves;
-  if (groups > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(chunk_kernel<DT>, dim3((unsigned)groups), dim3(kWaves * 64), 0, stream, a, chunks);
   if (a.parents != nullptr) {
     int32_t* token = reinterpret_cast<int32_t*>(static_cast<ChunkStat*>(a.workspace) + rows * chunks);
