@@ -134,12 +134,13 @@ struct Entries {
 
 // Entries with places in the pieces [lo, hi) into the lists of the threads that write them:
 // the piece's number modulo THREADS, or a row's last elements in order. What is made of a
-// list does not depend on its order.
+// list does not depend on its order. Entries without mass, as a padded list has them, change nothing and
+// stay out.
 template <int P, int THREADS>
 __device__ __forceinline__ void link(const DistillArgs& a, Teacher<THREADS>& s, int pieces, int64_t lo, int64_t hi) {
   for (int j = threadIdx.x; j < a.top_k; j += THREADS) {
     const int at = s.at[j], piece = at / P;
-    if (at < 0 || piece < lo || piece >= hi) continue;
+    if (at < 0 || piece < lo || piece >= hi || s.t[j] == 0.f) continue;
     s.next[j] = atomicExch(&s.head[piece < pieces ? piece % THREADS : at - pieces * P], j);
   }
 }
@@ -195,8 +196,15 @@ struct Writer {
       if (next < 0) {
         if (at / P == p) fix(x, g, at % P, t);
       } else {
-        for (int j = first; j >= 0; j = s.next[j])
-          if (s.at[j] / P == p) fix(x, g, s.at[j] % P, mass(s.at[j]));
+        // Each place once, so that a list of n entries of one place takes n steps a walk and not n^2 (1024
+        // entries at one place of 129280, 16 rows: 138 ms before).
+        uint32_t done = 0;
+        for (int j = first; j >= 0; j = s.next[j]) {
+          const int place = s.at[j], c = place % P;
+          if (place / P != p || (done >> c) & 1) continue;
+          done |= 1u << c;
+          fix(x, g, c, mass(place));
+        }
       }
     }
     return Elem<DT>::pack(g);
