@@ -312,9 +312,9 @@ def verify_tree(logits, tokens, parents, u, temperature=None):
     torch = _torch()
     fit = False
     try:
-        fit, (batch, nodes, vocab) = _drafts_fit(torch, logits, tokens, u, temperature)
-        fit = fit and (parents.dtype is torch.int32 and parents.shape == (batch, nodes) and parents.is_contiguous()
-                       and parents.get_device() == logits.get_device())
+        drafts, (batch, nodes, vocab) = _drafts_fit(torch, logits, tokens, u, temperature)
+        fit = drafts and (parents.dtype is torch.int32 and parents.shape == (batch, nodes) and parents.is_contiguous()
+                          and parents.get_device() == logits.get_device())
     except (AttributeError, IndexError, RuntimeError, ValueError):
         pass
     if not fit:
@@ -346,9 +346,9 @@ def verify_chain(logits, tokens, q, u, temperature=None):
     torch = _torch()
     fit = False
     try:
-        fit, (batch, nodes, vocab) = _drafts_fit(torch, logits, tokens, u, temperature)
-        fit = fit and (q.dtype is torch.float32 and q.shape == (batch, nodes - 1, vocab) and q.stride(2) == 1
-                       and q.get_device() == logits.get_device())
+        drafts, (batch, nodes, vocab) = _drafts_fit(torch, logits, tokens, u, temperature)
+        fit = drafts and (q.dtype is torch.float32 and q.shape == (batch, nodes - 1, vocab) and q.stride(2) == 1
+                          and q.get_device() == logits.get_device())
     except (AttributeError, IndexError, RuntimeError, ValueError):
         pass
     if not fit:
