@@ -118,3 +118,25 @@ def test_one_tensor_elsewhere(machine, name):  # noqa: F811
         for elsewhere, message in ((Far, "one GPU"), (torch.Tensor, "on the GPU")):
             args = {m: t.as_subclass(elsewhere if m == n else Near) for m, t in make().items()}
             assert message in (refusal(call, args) or ""), n
+
+
+def near(make, **change):
+    return {n: t.as_subclass(Near) for n, t in (make() | change).items()}
+
+
+def test_sizes_beyond_32_bits(machine):  # noqa: F811
+    cache = torch.zeros(1, 16, 2, 64, dtype=bf).expand(2 ** 31, 16, 2, 64)
+    for call, make in ((tq.tree_attention, attention), (tq.cache_append, append)):
+        with pytest.raises(ValueError, match="range"):
+            call(**near(make, k_cache=cache, v_cache=cache))
+    far_row = torch.empty(1, 1, 2 ** 32 + 50, dtype=torch.float16)  # never touched
+    small = dict(tokens=torch.zeros(1, 1, dtype=i32), u=torch.zeros(1, 1))
+    with pytest.raises(ValueError, match="below 2"):
+        tq.verify_tree(**near(dict, logits=far_row, parents=torch.zeros(1, 1, dtype=i32), **small))
+    with pytest.raises(ValueError, match="below 2"):
+        tq.verify_chain(**near(dict, logits=far_row, q=torch.empty(1, 0, 2 ** 32 + 50), **small))
+    for call, make in ((tq.distill, both), (tq.distill_loss, loss), (tq.distill_grad, both)):
+        args = {n: t[:1] for n, t in make().items()} | dict(logits=far_row[0])
+        with pytest.raises(ValueError, match="below 2"):
+            call(**near(dict, **args))
+    assert machine.calls == []

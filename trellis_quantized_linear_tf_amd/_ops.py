@@ -128,6 +128,19 @@ _ATTENTION = struct.Struct("@9if10QN19q")
 _APPEND = struct.Struct("@8i8Q13q")
 
 
+def _pack(layout, args, *values):
+    try:
+        layout.pack_into(args, 0, *values)
+    except (OverflowError, struct.error):
+        raise ValueError("a size, stride or scale is out of the library's range") from None
+
+
+def _sizes(*sizes):
+    """Numbers that the library takes as 32-bit integers."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes must be below 2^31, not {max(sizes)}")
+
+
 def _check_cache(k_cache, v_cache, table, lengths, dtypes, batch, heads, dim):
     torch = _torch()
     _need("k_cache", k_cache, 4, dtypes, (None, None, heads, dim))
@@ -203,11 +216,11 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
     a = _lib.TreeAttentionArgs(_dt_code(t), batch, nodes, hq, hkv, dim, pages[0], pages[1], columns)
     need = lib.tf_exl3_tree_attention_workspace(a)
     ws = _workspace(need, q)
-    _ATTENTION.pack_into(
-        a, 0, a.dtype, batch, nodes, hq, hkv, dim, pages[0], pages[1], columns, dim ** -0.5 if scale is None else scale,
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), need, *sq[:3], *sk[:3], *sv[:3],
-        *skc[:3], *svc[:3], *out.stride()[:3], table.stride(0))
+    _pack(
+        _ATTENTION, a, a.dtype, batch, nodes, hq, hkv, dim, pages[0], pages[1], columns,
+        dim ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), mask.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), need,
+        *sq[:3], *sk[:3], *sv[:3], *skc[:3], *svc[:3], *out.stride()[:3], table.stride(0))
     _run(q, lib.tf_exl3_tree_attention, a)
     if _followed(q, k, v, k_cache, v_cache):
         return _nodes()[0].apply("tree_attention", out, q, k, v, k_cache, v_cache)
@@ -266,8 +279,8 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None
     if dev < 0:
         _check_cache_append(k, v, k_cache, v_cache, table, lengths, nodes, counts)
     a = _lib.CacheAppendArgs()
-    _APPEND.pack_into(
-        a, 0, k.element_size(), batch, tokens, heads, dim, pages[0], pages[1], columns, k.data_ptr(), v.data_ptr(),
+    _pack(
+        _APPEND, a, k.element_size(), batch, tokens, heads, dim, pages[0], pages[1], columns, k.data_ptr(), v.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), _ptr(nodes) or 0, _ptr(counts) or 0,
         *sk[:3], *sv[:3], *skc[:3], *svc[:3], table.stride(0))
     _run(k, load().tf_exl3_cache_append, a)
@@ -322,6 +335,7 @@ def verify_tree(logits, tokens, parents, u, temperature=None):
         _need("parents", parents, 2, (torch.int32,), (batch, nodes))
         _whole("parents", parents)
         _one_gpu(logits, tokens, parents, u, temperature)
+    _sizes(batch, nodes, vocab)
     accepted = tokens.new_empty((batch, nodes))
     count, after = tokens.new_empty((batch,)), tokens.new_empty((batch,))
     lib = load()
@@ -355,6 +369,7 @@ def verify_chain(logits, tokens, q, u, temperature=None):
         batch, nodes, vocab = _check_drafts(logits, tokens, u, temperature)
         _need("q", q, 3, (torch.float32,), (batch, max(nodes - 1, 0), vocab))
         _one_gpu(logits, tokens, q, u, temperature)
+    _sizes(batch, nodes, vocab)
     count, after = tokens.new_empty((batch,)), tokens.new_empty((batch,))
     lib = load()
     need = lib.tf_exl3_verify_workspace(batch, nodes, vocab)
@@ -393,6 +408,7 @@ def _distill(logits, index, top, weight, temperature, want_loss, want_grad):
             _need("weight", weight, 1, (torch.float32,), (rows,))
             _whole("weight", weight)
         _one_gpu(logits, index, top, weight)
+    _sizes(rows, vocab, index.shape[1])
     loss = torch.empty((rows,), dtype=torch.float32, device=logits.device) if want_loss else None
     grad = logits.new_empty((rows, vocab)) if want_grad else None
     lib = load()
