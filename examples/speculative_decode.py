@@ -7,7 +7,8 @@ Each step drafts a tree with a small drafter, runs the tree's nodes through the 
 once (project, tree_attention), keeps the path that the model's own samples follow
 (verify_tree), puts that path's keys and values into the paged cache (cache_append), and
 teaches the drafter the model's top logits (distill). With temperature 0 the tokens are
-those of decoding one by one. Weights are random; the projections are 4-bit trellis streams.
+those of decoding one by one, but where logits tie within the order of attention's fp32 sums,
+which goes by the tree and the batch. Weights are random; the projections are 4-bit trellis streams.
 """
 
 import argparse

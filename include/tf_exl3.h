@@ -293,9 +293,9 @@ int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int 
  * over a dimension of 1 is not looked at. What lives on the device (lengths, page numbers, masks, node numbers, parents,
  * tokens) cannot be refused on the host: every kernel bounds it before an
  * address is made of it, as stated at each call. Sizes whose launches would have 2^32
- * work-items or more are refused (TF_E_SIZE) before the first launch. A workspace belongs to one call
- * at a time, needs no initial contents and may be used again, or freed in
- * stream order, after the call.
+ * work-items or more are refused (TF_E_SIZE) before the first launch. A workspace
+ * belongs to one call at a time, needs no initial contents and may be used again, or
+ * freed in stream order, after the call.
  */
 
 /*
@@ -311,8 +311,9 @@ int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int 
  * summed in fp32; probabilities are rounded to the inputs' type for the second
  * product: half an ulp each, and in fp16, for one below 2^-27 of the row's largest, up to
  * 2^-38 of that largest. Their sum and the output stay in fp32 until the one rounding of
- * the output. A value that no node may see never
- * reaches an output, infinities and NaN included.
+ * the output. A value that no node may see never reaches an output, infinities and NaN
+ * included. The same call gives the same bits; the order of a row's fp32 sums goes by
+ * the batch's lengths, table_pages and nodes.
  *
  * Position p of sequence b is slot p % page_size of page table[b][p / page_size].
  * lengths[b] is taken as 0 below 0 and as table_pages * page_size above that; a

@@ -132,7 +132,7 @@ def _pack(layout, args, *values):
     try:
         layout.pack_into(args, 0, *values)
     except (OverflowError, struct.error):
-        raise ValueError("a size, stride or scale is out of the library's range") from None
+        raise ValueError("a size or stride is out of the library's range") from None
 
 
 def _sizes(*sizes):

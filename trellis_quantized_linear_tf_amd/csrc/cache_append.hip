@@ -1,7 +1,8 @@
 // Rows of keys and values into a paged cache, byte for byte. Nothing is computed, so the
 // bytes, read once and written once, are the whole cost: every thread has kCopies
 // independent loads in flight before its first store. 32768 tokens of 8 heads of 128, bf16 keys
-// and values into pages: 268 MB read and written in 57 us, 4.7 TB/s (element by element 107).
+// and values into pages: 268 MB read and written in 57 us, 4.7 TB/s (element by element 107). The times at the
+// rule below are of inputs that stay in the caches from pass to pass: 45 us for the same tokens.
 #include "ops_device.hpp"
 #include "ops_launch.hpp"
 

@@ -17,17 +17,17 @@
 // says how far down fp16 holds that).
 //
 // All tiles of all sequences, heads and row tiles stand in one line, which the workgroups,
-// as many as the chip holds at a time, cut into pieces of equal time, whatever the lengths are:
+// as many as the chip holds at a time at 128 columns, cut into pieces of equal time, whatever the lengths are:
 // every workgroup finds its piece from the lengths on the device. Where a piece ends within a
 // sequence's tiles, it leaves fp32 outputs with their base and sum, and a second kernel
 // joins them.
 //
 // Few rows a key: bound by the cache's bytes. 32 sequences of 16384 positions, 16 nodes, 32
-// heads over 8 of 128, bf16: 2.14 GB in 392 us, 5.5 TB/s (keys and values two or three tiles
-// ahead, 64 to 128 KB a CU; with one tile ahead 496 us). Many rows a key: bound by the vector
-// and matrix instructions, whose times add on this chip: 4 trees of 64 nodes, 48 heads over
-// 8, up to 8191 positions: 66 us, 490 TFLOP/s; of its tile's time about 0.3 are matrix
-// products, 0.35 exponentials and sums, 0.2 shared memory, the rest barriers and loads. Taking
+// heads over 8 of 128, bf16: 2.14 GB in 393 us, 5.5 TB/s (keys and values two or three tiles
+// ahead, 64 to 128 KB a CU; with one tile ahead 496 us). Many rows a key: 4 trees of 64 nodes, 48
+// heads over 8, up to 8191 positions: 67 us, 480 TFLOP/s, 10 of them the second launch. Of the first's
+// cycles matrix products take 0.24, other vector instructions 0.28, exponentials' quarter rate 0.09; the rest
+// are barriers, of which one tile in shared memory needs two a tile, and waits for shared memory and loads. Taking
 // one row tile's exponentials between another's products, two row tiles a wave, or
 // independent workgroups of half the size measured 3 to 10% slower.
 #include <math.h>
@@ -735,7 +735,9 @@ namespace {
 // How a call's rows and positions are spread; by the sizes alone.
 struct Shape {
   int dp, rt, rg, kg, kw;
-  int resident;  // workgroups that a CU holds
+  // Workgroups a CU that the line is cut for: what a CU holds at 128 columns. (At 64 the registers allow
+  // twice as many, at 256 and up to 32 rows one.)
+  int resident;
   int tile() const { return kg * kw; }
   int rows() const { return 16 * rt * rg; }
 };

@@ -165,8 +165,8 @@ __device__ __forceinline__ const typename Elem<DT>::type* row_of(const VerifyArg
 }
 
 // One wave per chunk of every row. Bound by the fp64 rate: some 17 full-rate operations
-// a logit against 2 or 4 bytes: 768 rows of 129280 bf16 57 us (by a polynomial of degree 9 and no
-// table 62, with 98% of the cycles issuing vector instructions); 512 rows of fp32 43 us, 6.1 TB/s.
+// a logit against 2 or 4 bytes: 768 rows of 129280 bf16 58 us (by a polynomial of degree 9 and no
+// table 62, with 98% of the cycles issuing vector instructions); 512 rows of fp32 44 us, 6.0 TB/s.
 // Workgroups of 8 or 16 waves, or several chunks a wave, share the table more and measured
 // 58 to 63 us.
 template <int DT>
