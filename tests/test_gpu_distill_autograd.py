@@ -57,3 +57,27 @@ def test_both_results_and_a_second_backward(gpu):
         x.add_(1.0)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         again.backward()
+
+
+@pytest.mark.parametrize("both", [False, True])
+def test_the_backward_pass_takes_the_gradients_memory_alone(gpu, both):
+    """No gradient of the gradient's size beside it."""
+    x, index, top, w = (t.cuda() for t in inputs(11, 64, 50257, 20, "bf16"))
+    x.requires_grad_()
+    loss = tq.distill(x, index, top, w)[0] if both else tq.distill_loss(x, index, top)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    loss.sum().backward()
+    torch.cuda.synchronize()
+    size = x.numel() * x.element_size()
+    assert torch.cuda.max_memory_allocated() - before < 1.5 * size
+
+
+def test_a_loss_that_nothing_uses(gpu):
+    x, index, top, _ = (t.cuda() for t in inputs(12, 3, 100, 5, "f32"))
+    x.requires_grad_()
+    tq.distill_loss(x, index, top)
+    y = (x * 2).sum()
+    y.backward()
+    assert (x.grad == 2).all()

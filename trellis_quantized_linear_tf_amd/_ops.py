@@ -102,6 +102,7 @@ def _nodes():
     class DistillLoss(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, index, top, weight, temperature, want_grad):
+            ctx.set_materialize_grads(False)  # a gradient's gradient would be as large as the logits
             ctx.save_for_backward(logits, index, top)
             ctx.temperature = temperature
             loss, grad = _distill(logits, index, top, weight, temperature, True, want_grad)
@@ -112,6 +113,8 @@ def _nodes():
         @staticmethod
         @once_differentiable
         def backward(ctx, weight, _):
+            if weight is None:
+                return (None,) * 6
             if ctx.needs_input_grad[2]:
                 raise RuntimeError("the distillation loss has no gradient by the teacher's logits: pass top.detach()")
             logits, index, top = ctx.saved_tensors
