@@ -451,6 +451,152 @@ int tf_exl3_distill(int dtype, int rows, int vocab, int top_k, const void* logit
                     void* stream);
 size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k);
 
+/*
+ * Operators between the projection's rows and the cache: the norm of queries and keys
+ * with their rotation by position, attention of whole prompts, and a paged cache in 4
+ * bits: its append, its reading and the attention over it. Conventions as above.
+ */
+
+/*
+ * norm_rotate: each head's row of queries and keys, normed and turned by its token's
+ * position, in one pass.
+ *
+ *   y[d] = x[d] * r * w[d],  r = 1 / sqrt(mean_d x[d]^2 + eps)     (norm 0: y = x)
+ *   out[d1] = cast( y[d1] cos t - y[d2] sin t ),  out[d2] = cast( y[d1] sin t + y[d2] cos t )
+ *
+ * with t = positions[b][i] * frequencies[f] radians for the pairs (d1, d2) = (f, f +
+ * rotary_dim / 2), or (2f, 2f + 1) where interleaved, f < rotary_dim / 2; elements from
+ * rotary_dim on are y, cast. Sums and products are in fp32, rounded once to the type at the
+ * end; t is formed and reduced to a part of a turn in 64 bits, so far positions keep
+ * fp32's accuracy.
+ * A row's squares are summed in fp32: elements past about 10^18 make a row of zeros.
+ *
+ *   dtype        of q, k and the outputs; weight_dtype of q_weight and k_weight (each
+ *                [head_dim] or NULL: all ones); any of the three
+ *   q, k         [batch][tokens][heads][head_dim], strides [batch, token, head]
+ *   q_out, k_out likewise; each may be its input itself (the same pointer and strides), else
+ *                they overlap no input; rows of q and k may alternate in one buffer
+ *   positions    int32 [batch][tokens], rows positions_stride apart
+ *   frequencies  fp32 [rotary_dim / 2] (NULL if rotary_dim is 0)
+ *   head_dim     a multiple of 16 up to 512; rotary_dim a multiple of 16 up to head_dim
+ *   batch * tokens below 2^24
+ */
+typedef struct tf_exl3_norm_rotate_args {
+  int dtype, weight_dtype, batch, tokens, q_heads, kv_heads, head_dim, rotary_dim;
+  int interleaved, norm;
+  float eps;
+  const void *q, *k;
+  const void *q_weight, *k_weight;
+  const int32_t* positions;
+  const float* frequencies;
+  void *q_out, *k_out;
+  int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+  int64_t positions_stride;
+} tf_exl3_norm_rotate_args;
+
+int tf_exl3_norm_rotate(const tf_exl3_norm_rotate_args* a, void* stream);
+
+/*
+ * prompt_attention: causal attention of whole prompts that are packed behind one another.
+ * Sequence b has the tokens offsets[b] .. offsets[b + 1] - 1; its token i sees its tokens
+ * up to i:
+ *
+ *   x[j] = scale * sum_d q[i][h][d] * k[j][g][d],   g = h / (q_heads / kv_heads)
+ *   out[i][h] = cast( sum_j exp(x[j] - max x) v[j][g] / sum_j exp(x[j] - max x) ),  offsets[b] <= j <= i
+ *
+ * Numerics as in tree_attention. Rows of out in front of offsets[0] and from
+ * offsets[batch] on are left as they were, whatever q, k and v hold there. Offsets are
+ * taken within [0, tokens]; where they do not ascend, rows are not as stated, but no
+ * address leaves its buffer. The same call gives the same bits; a row's do not depend on
+ * other sequences but through where its own begins within a tile of tokens.
+ *
+ *   dtype     TF_DT_F16 or TF_DT_BF16
+ *   head_dim  a multiple of 16, up to 256; q_heads a multiple of kv_heads
+ *   tokens    rows of q, k, v and out, below 2^30; batch below 2^30
+ *   offsets   int32 [batch + 1]
+ *   strides   [token, head], multiples of 8 elements, those of k and v over tokens at most 2^23,
+ *             pointers 16-byte aligned (out: 4 elements, 8 bytes)
+ */
+typedef struct tf_exl3_prompt_attention_args {
+  int dtype, tokens, batch, q_heads, kv_heads, head_dim;
+  float scale;
+  const void *q, *k, *v;
+  const int32_t* offsets;
+  void* out;
+  int64_t q_stride[2], k_stride[2], v_stride[2], out_stride[2];
+} tf_exl3_prompt_attention_args;
+
+int tf_exl3_prompt_attention(const tf_exl3_prompt_attention_args* a, void* stream);
+
+/*
+ * A cache in 4 bits. A row of head_dim numbers x is kept in groups of 32:
+ *
+ *   x as fp32, NaN as 0, within [-65504, 65504]
+ *   m = RN16(min x) (never -0),  s = RN16(RN32((max x - min x) / 15))
+ *   n[i] = rint(RN32(RN32(x[i] - m) / s)) within 0 .. 15 (ties to even), 0 where s is 0
+ *
+ * and stands for n * s + m: rounded to the type that is asked for, by way of fp32 in bf16. Its
+ * tf_exl3_q4_row_bytes(head_dim) = 5 head_dim / 8 bytes are the codes, then a pair (s, m) of fp16
+ * for each group. Eight codes are a little-endian 32-bit word: bits 4i .. 4i + 3 hold
+ * number 2i of the eight, bits 16 + 4i .. 19 + 4i number 2i + 1.
+ * head_dim is a multiple of 32. Strides of caches are in BYTES, multiples of 4; pointers
+ * are 4-byte aligned. Rows that lie behind one another by position, the heads' pages apart,
+ * are read in whole cache lines; with the heads of a slot together a head's row is part of
+ * two, which attention reads from HBM more than once.
+ */
+size_t tf_exl3_q4_row_bytes(int head_dim); /* 0 where head_dim is refused */
+
+/*
+ * cache_append_q4: rows of k and v into a cache in 4 bits; positions, nodes, counts and what
+ * is left out as in cache_append. Two rows of one call that go to the same slot leave a
+ * mixture of them there.
+ *
+ *   dtype    of k and v, any of the three; strides in elements, any alignment of whole ones
+ */
+typedef struct tf_exl3_cache_append_q4_args {
+  int dtype, batch, tokens, kv_heads, head_dim;
+  int pages, page_size, table_pages;
+  const void *k, *v;
+  void *k_cache, *v_cache;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* nodes;   /* [batch][tokens] or NULL */
+  const int32_t* counts;  /* [batch] or NULL */
+  int64_t k_stride[3], v_stride[3], k_cache_stride[3], v_cache_stride[3];
+  int64_t table_stride;
+} tf_exl3_cache_append_q4_args;
+
+int tf_exl3_cache_append_q4(const tf_exl3_cache_append_q4_args* a, void* stream);
+
+/*
+ * cache_read_q4: what positions first[b] + j, j < tokens, of sequence b stand for (first NULL:
+ * from 0). Rows of positions below 0 or from lengths[b] on, outside the table or on a page
+ * outside [0, pages) are zeros.
+ *
+ *   dtype    of k and v, any of the three; strides in elements, any alignment of whole ones
+ */
+typedef struct tf_exl3_cache_read_q4_args {
+  int dtype, batch, tokens, kv_heads, head_dim;
+  int pages, page_size, table_pages;
+  const void *k_cache, *v_cache;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* first;   /* [batch] or NULL */
+  void *k, *v;
+  int64_t k_cache_stride[3], v_cache_stride[3], k_stride[3], v_stride[3];
+  int64_t table_stride;
+} tf_exl3_cache_read_q4_args;
+
+int tf_exl3_cache_read_q4(const tf_exl3_cache_read_q4_args* a, void* stream);
+
+/*
+ * tree_attention_q4: tree_attention whose cache is in 4 bits; the nodes' own k and v are
+ * of dtype, as q. A cached key or value is what cache_read_q4 gives in that type. head_dim is
+ * a multiple of 32 up to 256, k_cache_stride and v_cache_stride are in bytes.
+ */
+int tf_exl3_tree_attention_q4(const tf_exl3_tree_attention_args* a, void* stream);
+size_t tf_exl3_tree_attention_q4_workspace(const tf_exl3_tree_attention_args* a);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 """EXL3 decode-row projection for MI355X (gfx950): rot_in and the trellis linear, and
 the operators around it: attention of drafted trees over a paged cache, the cache's
-append, verification of the drafts and distillation of a drafter.
+append, verification of the drafts and distillation of a drafter; norms and rotation of
+queries and keys, attention of whole prompts, and a cache in 4 bits.
 
 The compute runs in libtf_exl3.so (hand-written HIP kernels behind the C ABI in
 include/tf_exl3.h); this package only marshals torch tensors and streams into
@@ -38,6 +39,14 @@ from ._ops import (  # noqa: F401
     tree_attention,
     verify_chain,
     verify_tree,
+)
+from ._rows import (  # noqa: F401
+    cache_append_q4,
+    cache_read_q4,
+    norm_rotate,
+    prompt_attention,
+    q4_row_bytes,
+    tree_attention_q4,
 )
 
 WIDTHS = (2, 3, 4, 5, 6, 8)

@@ -77,6 +77,44 @@ class CacheAppendArgs(ctypes.Structure):
     ]
 
 
+class CacheAppendQ4Args(ctypes.Structure):
+    _fields_ = [
+        *((n, _I) for n in ("dtype", "batch", "tokens", "kv_heads", "head_dim", "pages", "page_size", "table_pages")),
+        *((n, _P) for n in ("k", "v", "k_cache", "v_cache", "table", "lengths", "nodes", "counts")),
+        *((n, _L * 3) for n in ("k_stride", "v_stride", "k_cache_stride", "v_cache_stride")),
+        ("table_stride", _L),
+    ]
+
+
+class CacheReadQ4Args(ctypes.Structure):
+    _fields_ = [
+        *((n, _I) for n in ("dtype", "batch", "tokens", "kv_heads", "head_dim", "pages", "page_size", "table_pages")),
+        *((n, _P) for n in ("k_cache", "v_cache", "table", "lengths", "first", "k", "v")),
+        *((n, _L * 3) for n in ("k_cache_stride", "v_cache_stride", "k_stride", "v_stride")),
+        ("table_stride", _L),
+    ]
+
+
+class NormRotateArgs(ctypes.Structure):
+    _fields_ = [
+        *((n, _I) for n in ("dtype", "weight_dtype", "batch", "tokens", "q_heads", "kv_heads", "head_dim", "rotary_dim",
+                            "interleaved", "norm")),
+        ("eps", _F),
+        *((n, _P) for n in ("q", "k", "q_weight", "k_weight", "positions", "frequencies", "q_out", "k_out")),
+        *((n, _L * 3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")),
+        ("positions_stride", _L),
+    ]
+
+
+class PromptAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        *((n, _I) for n in ("dtype", "tokens", "batch", "q_heads", "kv_heads", "head_dim")),
+        ("scale", _F),
+        *((n, _P) for n in ("q", "k", "v", "offsets", "out")),
+        *((n, _L * 2) for n in ("q_stride", "k_stride", "v_stride", "out_stride")),
+    ]
+
+
 SIGNATURES = {
     "tf_exl3_rot_in": (_I, [_P, _I, _P, _P, _I, _I, _P]),
     "tf_exl3_linear": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P]),
@@ -101,6 +139,13 @@ SIGNATURES = {
     "tf_exl3_verify_workspace": (_Z, [_I, _I, _I]),
     "tf_exl3_distill": (_I, [_I, _I, _I, _I, _P, _L, _P, _P, _I, _P, _F, _P, _P, _L, _P, _Z, _P]),
     "tf_exl3_distill_workspace": (_Z, [_I, _I, _I, _I]),
+    "tf_exl3_norm_rotate": (_I, [ctypes.POINTER(NormRotateArgs), _P]),
+    "tf_exl3_prompt_attention": (_I, [ctypes.POINTER(PromptAttentionArgs), _P]),
+    "tf_exl3_q4_row_bytes": (_Z, [_I]),
+    "tf_exl3_cache_append_q4": (_I, [ctypes.POINTER(CacheAppendQ4Args), _P]),
+    "tf_exl3_cache_read_q4": (_I, [ctypes.POINTER(CacheReadQ4Args), _P]),
+    "tf_exl3_tree_attention_q4": (_I, [ctypes.POINTER(TreeAttentionArgs), _P]),
+    "tf_exl3_tree_attention_q4_workspace": (_Z, [ctypes.POINTER(TreeAttentionArgs)]),
     "tf_exl3_calib_copy": (_I, [_P, _P, ctypes.c_size_t, _I, _P]),
     "tf_exl3_calib_stream_read": (_I, [_P, ctypes.c_size_t, _P, _I, _P]),
 }

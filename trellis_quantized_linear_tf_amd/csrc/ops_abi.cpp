@@ -1,69 +1,26 @@
 // C ABI of the operators around the projection: argument checks on the host, then one
 // call into the launch interface. Nothing is launched or written on a refusal.
 #include <math.h>
-#include <stddef.h>
-#include <stdint.h>
 
+#include "ops_check.hpp"
 #include "ops_launch.hpp"
-#include "tf_exl3.h"
+
+using namespace tf_exl3;
 
 namespace {
 
-constexpr int kMaxBatch = 65535;        // sequences, a grid dimension
 constexpr int kMaxTreeNodes = 64;       // bits of a node's mask
 constexpr int kMaxVerifyNodes = 1024;
 constexpr int kMaxTop = 1024;           // the teacher's entries, held in shared memory
-constexpr int64_t kMaxStride = 1ll << 40;
 
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-
-size_t elem_size(int dt) { return dt == TF_DT_F32 ? 4 : 2; }
-
-bool dtype_ok(int dt) { return dt == TF_DT_F32 || dt == TF_DT_F16 || dt == TF_DT_BF16; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (na == 0 || nb == 0 || a == nullptr || b == nullptr) return false;
-  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
-// Bytes from the first to past the last element of [n0][n1][n2][d] with strides s.
-size_t extent(int64_t n0, int64_t n1, int64_t n2, int64_t d, const int64_t* s, size_t elem) {
-  return (size_t)((n0 - 1) * s[0] + (n1 - 1) * s[1] + (n2 - 1) * s[2] + d) * elem;
-}
-
-// A stride over a dimension of 1 is never used, whatever it is.
-void settle(int64_t n0, int64_t n1, int64_t n2, int64_t* s) {
-  if (n0 <= 1) s[0] = 0;
-  if (n1 <= 1) s[1] = 0;
-  if (n2 <= 1) s[2] = 0;
-}
-
-bool strides_ok(const int64_t* s, int64_t multiple) {
-  for (int i = 0; i < 3; ++i)
-    if (s[i] < 0 || s[i] > kMaxStride || s[i] % multiple != 0) return false;
-  return true;
-}
-
-// Rows that are written may not share elements: no stride of 0 over more than one of them.
-bool apart(int64_t n0, int64_t n1, int64_t n2, const int64_t* s) {
-  return (n0 <= 1 || s[0] != 0) && (n1 <= 1 || s[1] != 0) && (n2 <= 1 || s[2] != 0);
-}
-
-int cache_sizes(int pages, int page_size, int table_pages, int64_t table_stride) {
-  if (pages < 1 || page_size < 1 || table_pages < 0 || table_stride < 0 || table_stride > kMaxStride) return TF_E_SIZE;
-  // Positions are 32-bit: room for the longest sequence and its new tokens.
-  if ((int64_t)table_pages * page_size > (1ll << 30)) return TF_E_SIZE;
-  return TF_OK;
-}
-
-int attention_sizes(const tf_exl3_tree_attention_args* a) {
+int attention_sizes(const tf_exl3_tree_attention_args* a, bool q4) {
   if (a->dtype != TF_DT_F16 && a->dtype != TF_DT_BF16) return TF_E_DTYPE;
   if (a->batch < 0 || a->batch > kMaxBatch || a->nodes < 1 || a->nodes > kMaxTreeNodes) return TF_E_SIZE;
   if (a->kv_heads < 1 || a->q_heads < 1 || a->q_heads > kMaxBatch || a->q_heads % a->kv_heads != 0) return TF_E_SIZE;
-  if (a->head_dim < 16 || a->head_dim > 256 || a->head_dim % 16 != 0) return TF_E_SIZE;
+  if (a->head_dim < 16 || a->head_dim > 256 || a->head_dim % (q4 ? 32 : 16) != 0) return TF_E_SIZE;
   const int st = cache_sizes(1, a->page_size, a->table_pages, 0);
-  return st != TF_OK || tf_exl3::tree_attention_fits(*a) ? st : TF_E_SIZE;
+  if (st != TF_OK) return st;
+  return (q4 ? tree_attention_q4_fits(*a) : tree_attention_fits(*a)) ? TF_OK : TF_E_SIZE;
 }
 
 int verify_sizes(int batch, int nodes, int vocab, bool tree) {
@@ -75,16 +32,8 @@ bool row_strides_ok(int64_t batch, int64_t node) {
   return batch >= 0 && node >= 0 && batch <= kMaxStride && node <= kMaxStride;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t tf_exl3_tree_attention_workspace(const tf_exl3_tree_attention_args* a) {
-  if (a == nullptr || attention_sizes(a) != TF_OK) return 0;
-  return tf_exl3::tree_attention_workspace(*a);
-}
-
-int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* args, void* stream) {
+// Both forms of the cache: rows of 16-bit elements, strides in elements; or in 4 bits (q4), strides in bytes.
+int tree_attention(const tf_exl3_tree_attention_args* args, bool q4, void* stream) {
   if (args == nullptr) return TF_E_NULL;
   tf_exl3_tree_attention_args settled = *args;
   tf_exl3_tree_attention_args* a = &settled;
@@ -94,29 +43,30 @@ int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* args, void* stream
   settle(a->pages, a->page_size, a->kv_heads, a->k_cache_stride);
   settle(a->pages, a->page_size, a->kv_heads, a->v_cache_stride);
   settle(a->batch, a->nodes, a->q_heads, a->out_stride);
-  int st = attention_sizes(a);
+  int st = attention_sizes(a, q4);
   if (st == TF_OK) st = cache_sizes(a->pages, a->page_size, a->table_pages, a->table_stride);
   if (st != TF_OK) return st;
   if (!isfinite(a->scale)) return TF_E_SIZE;
   if (!strides_ok(a->q_stride, 8) || !strides_ok(a->k_stride, 8) || !strides_ok(a->v_stride, 8) ||
-      !strides_ok(a->k_cache_stride, 8) || !strides_ok(a->v_cache_stride, 8) || !strides_ok(a->out_stride, 4) ||
+      !strides_ok(a->k_cache_stride, q4 ? 4 : 8) || !strides_ok(a->v_cache_stride, q4 ? 4 : 8) || !strides_ok(a->out_stride, 4) ||
       !apart(a->batch, a->nodes, a->q_heads, a->out_stride))
     return TF_E_SIZE;
   if (a->batch == 0) return TF_OK;
   if (!a->q || !a->k || !a->v || !a->mask || !a->k_cache || !a->v_cache || !a->lengths || !a->out || !a->workspace ||
       (a->table_pages > 0 && !a->table))
     return TF_E_NULL;
-  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->k_cache, 16) ||
-      !aligned(a->v_cache, 16) || !aligned(a->out, 8) || !aligned(a->workspace, 16) || !aligned(a->mask, 8) ||
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->k_cache, q4 ? 4 : 16) ||
+      !aligned(a->v_cache, q4 ? 4 : 16) || !aligned(a->out, 8) || !aligned(a->workspace, 16) || !aligned(a->mask, 8) ||
       !aligned(a->table, 4) || !aligned(a->lengths, 4))
     return TF_E_ALIGN;
-  const size_t need = tf_exl3::tree_attention_workspace(*a);
+  const size_t need = q4 ? tree_attention_q4_workspace(*a) : tree_attention_workspace(*a);
   if (a->workspace_bytes < need) return TF_E_WORKSPACE;
   const size_t rows_q = extent(a->batch, a->nodes, a->q_heads, a->head_dim, a->q_stride, 2);
   const size_t rows_k = extent(a->batch, a->nodes, a->kv_heads, a->head_dim, a->k_stride, 2);
   const size_t rows_v = extent(a->batch, a->nodes, a->kv_heads, a->head_dim, a->v_stride, 2);
-  const size_t kc = extent(a->pages, a->page_size, a->kv_heads, a->head_dim, a->k_cache_stride, 2);
-  const size_t vc = extent(a->pages, a->page_size, a->kv_heads, a->head_dim, a->v_cache_stride, 2);
+  const int64_t row = q4 ? q4_bytes(a->head_dim) : a->head_dim;
+  const size_t kc = extent(a->pages, a->page_size, a->kv_heads, row, a->k_cache_stride, q4 ? 1 : 2);
+  const size_t vc = extent(a->pages, a->page_size, a->kv_heads, row, a->v_cache_stride, q4 ? 1 : 2);
   const size_t no = extent(a->batch, a->nodes, a->q_heads, a->head_dim, a->out_stride, 2);
   const void* written[2] = {a->out, a->workspace};
   const size_t bytes[2] = {no, need};
@@ -130,9 +80,26 @@ int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* args, void* stream
       return TF_E_ALIAS;
   }
   if (overlap(a->out, no, a->workspace, need)) return TF_E_ALIAS;
-  const hipError_t e = tf_exl3::launch_tree_attention(*a, static_cast<hipStream_t>(stream));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = q4 ? launch_tree_attention_q4(*a, s) : launch_tree_attention(*a, s);
   return e == hipSuccess ? TF_OK : TF_E_LAUNCH;
 }
+
+}  // namespace
+
+extern "C" {
+
+size_t tf_exl3_tree_attention_workspace(const tf_exl3_tree_attention_args* a) {
+  return a == nullptr || attention_sizes(a, false) != TF_OK ? 0 : tf_exl3::tree_attention_workspace(*a);
+}
+
+int tf_exl3_tree_attention(const tf_exl3_tree_attention_args* a, void* stream) { return tree_attention(a, false, stream); }
+
+size_t tf_exl3_tree_attention_q4_workspace(const tf_exl3_tree_attention_args* a) {
+  return a == nullptr || attention_sizes(a, true) != TF_OK ? 0 : tf_exl3::tree_attention_q4_workspace(*a);
+}
+
+int tf_exl3_tree_attention_q4(const tf_exl3_tree_attention_args* a, void* stream) { return tree_attention(a, true, stream); }
 
 int tf_exl3_cache_append(const tf_exl3_cache_append_args* args, void* stream) {
   if (args == nullptr) return TF_E_NULL;

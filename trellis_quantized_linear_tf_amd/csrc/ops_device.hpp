@@ -96,6 +96,33 @@ struct Elem<TF_DT_BF16> {
   }
 };
 
+// Eight elements of a row, at any alignment of whole ones.
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, float (&x)[8]) {
+  if constexpr (DT == TF_DT_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 v = load_piece(p + 4 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[4 * h + i] = bits_to_f32(v[i]);
+    }
+  } else {
+    Elem<DT>::unpack(load_piece(p), x);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(typename Elem<DT>::type* p, const float (&x)[8]) {
+  if constexpr (DT == TF_DT_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      store_piece(p + 4 * h, u32x4{f32_to_bits(x[4 * h]), f32_to_bits(x[4 * h + 1]), f32_to_bits(x[4 * h + 2]),
+                                   f32_to_bits(x[4 * h + 3])});
+  } else {
+    store_piece(p, Elem<DT>::pack(x));
+  }
+}
+
 __device__ __forceinline__ float load_elem(const void* p, int dtype, int64_t i) {
   if (dtype == TF_DT_F32) return static_cast<const float*>(p)[i];
   const uint16_t b = static_cast<const uint16_t*>(p)[i];

@@ -18,8 +18,23 @@ bool tree_attention_fits(const tf_exl3_tree_attention_args& a);
 hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream);
 size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a);
 
+// The same with a cache in 4 bits, whose strides are in bytes.
+bool tree_attention_q4_fits(const tf_exl3_tree_attention_args& a);
+hipError_t launch_tree_attention_q4(const tf_exl3_tree_attention_args& a, hipStream_t stream);
+size_t tree_attention_q4_workspace(const tf_exl3_tree_attention_args& a);
+
 bool cache_append_fits(const tf_exl3_cache_append_args& a);
 hipError_t launch_cache_append(const tf_exl3_cache_append_args& a, hipStream_t stream);
+
+bool cache_append_q4_fits(const tf_exl3_cache_append_q4_args& a);
+hipError_t launch_cache_append_q4(const tf_exl3_cache_append_q4_args& a, hipStream_t stream);
+bool cache_read_q4_fits(const tf_exl3_cache_read_q4_args& a);
+hipError_t launch_cache_read_q4(const tf_exl3_cache_read_q4_args& a, hipStream_t stream);
+
+hipError_t launch_norm_rotate(const tf_exl3_norm_rotate_args& a, hipStream_t stream);
+
+bool prompt_attention_fits(const tf_exl3_prompt_attention_args& a);
+hipError_t launch_prompt_attention(const tf_exl3_prompt_attention_args& a, hipStream_t stream);
 
 struct VerifyArgs {
   int dtype, batch, nodes, vocab;

@@ -1,0 +1,386 @@
+// Causal attention of whole prompts, packed behind one another.
+//
+// A workgroup takes a tile of kRows consecutive tokens of one query head, whatever sequences they
+// belong to: each row knows where its sequence begins, and sees the keys from there to itself. So short
+// sequences share a tile, and nothing has to be known of them on the host. The keys from the first row's
+// beginning to the last row are walked in tiles of KT that all waves load together, straight into shared
+// memory, one tile ahead; each of the four waves holds 16 RT rows.
+//
+// Products are transposed as in tree attention: S^T = K Q^T leaves a lane with 4 positions of one row
+// per tile of 16, and its weights are where O^T = V^T P^T wants them. Only tiles that some row of a wave does
+// not see as a whole are masked.
+#include <math.h>
+
+#include "attention_device.hpp"
+#include "ops_launch.hpp"
+
+namespace tf_exl3 {
+
+struct PromptPlan {
+  int tiles;           // of tokens
+  int spread;          // heads of an XCD, where all of them have equally many; else 0
+  float c, slack;      // |scale| log2(e); the type's slack in scores
+  bool negate;         // scale < 0
+  FastDiv by_heads, by_group;  // by_heads: spread, or q_heads
+};
+
+constexpr int kPromptWaves = 4, kPromptThreads = 64 * kPromptWaves;
+constexpr int kXCDs = 8;
+constexpr int kNowhere = 0x7FFFFFFF;  // the beginning of a row that belongs to no sequence
+
+// Where the sequence of token i begins; kNowhere in front of the first and behind the last one.
+__device__ __forceinline__ int sequence_begin(const int32_t* offsets, int batch, int i) {
+  int lo = -1, hi = batch + 1;  // offsets[lo] <= i < offsets[hi], as if there were such ends
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (offsets[mid] <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo < 0 || lo == batch ? kNowhere : max(offsets[lo], 0);
+}
+
+template <typename F>
+__device__ __forceinline__ int rows_reduce(int v, F f) {  // over the 16 rows that a lane group holds
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) v = f(v, __shfl_xor(v, s));
+  return v;
+}
+
+// Whether one of the 16-bit elements of a 16-byte piece is no finite number.
+template <int DT>
+__device__ __forceinline__ uint32_t largest_exponents(u32x4 v, uint32_t so_far) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = v[i] & 0x7FFF7FFFu;
+    so_far = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, u), __builtin_bit_cast(u16x2, so_far)));
+  }
+  return so_far;
+}
+
+// 16 bytes a lane, `offset` bytes from `base`, to shared memory at `to` + 16 lane (base and `to` the same
+// for all lanes). The load is not among those that the compiler counts: it is waited for with wait_loads before
+// the barrier behind which its bytes are read. (With the compiler's builtin every read of shared memory, of the
+// other half too, waited for the loads in flight.)
+__device__ __forceinline__ void load_to_shared(const void* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(to), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int DT, int DP, int RT, int KT>
+__global__ __launch_bounds__(kPromptThreads, 2) void prompt_attention_kernel(tf_exl3_prompt_attention_args a, PromptPlan p) {
+  typedef uint16_t T;
+  constexpr int NC = DP / 8, NK = KT / 16, NB = KT / 32, ND = DP / 16, NQ = DP / 32, kRows = 16 * RT * kPromptWaves;
+  constexpr int kTile = KT * NC, kStep = kPromptThreads / NC, kLoads = KT / kStep;
+  static_assert(KT % kStep == 0 && KT % 32 == 0, "");
+  __shared__ u32x4 lds[4 * kTile];  // keys and values of two tiles
+  __shared__ int ranges[2][kPromptWaves];
+
+  // The last tiles, which see most, come first; the heads of a kv head stay on one XCD where they can.
+  int tile, head;
+  {
+    const int id = blockIdx.x;
+    if (p.spread) {
+      const int slot = id / kXCDs, t = p.by_heads.div(slot);
+      tile = p.tiles - 1 - t, head = id % kXCDs * p.spread + slot - t * p.spread;
+    } else {
+      const int t = p.by_heads.div(id);
+      tile = p.tiles - 1 - t, head = id - t * a.q_heads;
+    }
+  }
+  const int g = p.by_group.div(head);
+  const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int row0 = tile * kRows + wave * 16 * RT;  // the wave's first token
+
+  // Rows, the beginnings of their sequences, and what the wave and the workgroup look at.
+  int begin[RT];
+  int low = kNowhere, high = 0, latest = 0;  // first key, past the last, latest beginning
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int i = row0 + rt * 16 + (lane & 15);
+    begin[rt] = i < a.tokens ? sequence_begin(a.offsets, a.batch, i) : kNowhere;
+    if (begin[rt] > i) begin[rt] = kNowhere;
+    low = min(low, begin[rt]), latest = max(latest, begin[rt]);
+    if (begin[rt] != kNowhere) high = max(high, i + 1);
+  }
+  low = __builtin_amdgcn_readfirstlane(rows_reduce(low, [](int x, int y) { return min(x, y); }));
+  high = __builtin_amdgcn_readfirstlane(rows_reduce(high, [](int x, int y) { return max(x, y); }));
+  latest = __builtin_amdgcn_readfirstlane(rows_reduce(latest, [](int x, int y) { return max(x, y); }));
+  if (lane == 0) ranges[0][wave] = low, ranges[1][wave] = high;
+
+  u32x4 q[RT][NQ];
+  {
+    const uint32_t flip = p.negate ? 0x80008000u : 0u;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int i = row0 + rt * 16 + (lane & 15);
+      const T* row = static_cast<const T*>(a.q) + i * a.q_stride[0] + head * a.q_stride[1];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const int d = n * 32 + lg * 8;
+        q[rt][n] = u32x4(0u);
+        if (begin[rt] != kNowhere && d < a.head_dim) q[rt][n] = *reinterpret_cast<const u32x4*>(row + d);
+        q[rt][n] ^= flip;
+      }
+    }
+  }
+  // Columns behind the head's are zero throughout.
+  if (a.head_dim < DP) {
+    for (int i = tid; i < 4 * kTile; i += kPromptThreads) lds[i] = u32x4(0u);
+  }
+  __syncthreads();
+  int from = ranges[0][0], to = ranges[1][0];
+#pragma unroll
+  for (int w = 1; w < kPromptWaves; ++w) from = min(from, ranges[0][w]), to = max(to, ranges[1][w]);
+  from = __builtin_amdgcn_readfirstlane(from), to = __builtin_amdgcn_readfirstlane(to);
+  if (from >= to) return;
+
+  const T* const kb = static_cast<const T*>(a.k) + g * a.k_stride[1];
+  const T* const vb = static_cast<const T*>(a.v) + g * a.v_stride[1];
+  // The loader's part: chunk tid % NC of rows tid / NC, + kStep, ... as shared memory has them. Of 8 rows
+  // between them (256 columns) two neighbours differ in the place of a key's chunk.
+  constexpr int kKinds = kStep < 16 ? 2 : 1;
+  const int chunk = tid % NC, lrow = tid / NC;
+  const uint32_t ks = (uint32_t)a.k_stride[0] * 2, vs = (uint32_t)a.v_stride[0] * 2;  // bytes, at most 2^24
+  const uint32_t place = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)lds + wave * 1024;
+  int kc[kKinds];
+#pragma unroll
+  for (int n = 0; n < kKinds; ++n) kc[n] = key_chunk<DP>(lrow + n * kStep, chunk);
+  const int vc = value_chunk<DP>(lrow, chunk);
+  auto stage = [&](int at, int buffer) {
+    const T* const kt = kb + (int64_t)at * a.k_stride[0];
+    const T* const vt = vb + (int64_t)at * a.v_stride[0];
+    const uint32_t dst = place + buffer * 2 * kTile * 16;
+    const int last = a.tokens - 1 - at;
+    if (last >= KT - 1) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int c = kc[n % kKinds];
+        if (c * 8 < a.head_dim)
+          load_to_shared(kt + (int64_t)n * kStep * a.k_stride[0], lrow * ks + c * 16, dst + n * kPromptThreads * 16);
+        if (vc * 8 < a.head_dim)
+          load_to_shared(vt + (int64_t)n * kStep * a.v_stride[0], lrow * vs + vc * 16, dst + (kTile + n * kPromptThreads) * 16);
+      }
+    } else {  // behind the last token its row again
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int c = kc[n % kKinds], row = min(lrow + n * kStep, last);
+        if (c * 8 < a.head_dim) load_to_shared(kt, row * ks + c * 16, dst + n * kPromptThreads * 16);
+        if (vc * 8 < a.head_dim) load_to_shared(vt, row * vs + vc * 16, dst + (kTile + n * kPromptThreads) * 16);
+      }
+    }
+  };
+
+  f32x4 o[ND][RT];
+  float m[RT], z[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY, z[rt] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) o[dt][rt] = f32x4(0.f);
+  }
+  const int key_row = (lane & 15) * NC;
+  const int vrow = lg * 4 + ((lane & 15) >> 2);  // of the 32 positions of a step, and 16 behind
+  const int value_row = kTile + vrow * NC;
+
+  stage(from, 0);
+  int half = 0;
+  for (int at = from; at < to; at += KT) {
+    wait_loads();     // this wave's part of the tile is there,
+    __syncthreads();  // and everyone's; the tile before is no longer in use
+    if (at + KT < to) stage(at + KT, half ^ 1);
+    if (at < high && at + KT > low) {
+      const u32x4* tile = lds + half * 2 * kTile;
+      const bool edge = at < latest || at + KT - 1 > row0;
+      // Scores relative to the row's base m, which the products are summed onto.
+      f32x4 s[NK][RT];
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[t][rt] = f32x4(m[rt] == -INFINITY ? 0.f : -m[rt]);
+      constexpr int kAhead = 2, kRing = kAhead + 1;
+      u32x4 kf[kRing];
+      auto key_operand = [&](int n) { return tile[key_row + n % NK * 16 * NC + key_chunk<DP>(lane & 15, n / NK * 4 + lg)]; };
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) kf[n] = key_operand(n);
+#pragma unroll
+      for (int n = 0; n < NQ * NK; ++n) {
+        if (n + kAhead < NQ * NK) kf[(n + kAhead) % kRing] = key_operand(n + kAhead);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[n % NK][rt] = mfma<DT>(kf[n % kRing], q[rt][n / NK], s[n % NK][rt]);
+        keep_order();
+      }
+
+      if (edge) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          // j is seen where begin <= j <= i: j - begin, as a number without a sign, is at most i - begin
+          const uint32_t span = begin[rt] == kNowhere ? 0u : (uint32_t)(row0 + rt * 16 + (lane & 15) - begin[rt]);
+#pragma unroll
+          for (int t = 0; t < NK; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t j = (uint32_t)(at + t * 16 + lg * 4 + i - begin[rt]);
+              s[t][rt][i] = j <= span ? s[t][rt][i] : -INFINITY;
+            }
+        }
+      }
+
+      // A row's base is raised only where one of its scores has grown past it by the type's slack, whatever
+      // the other rows of the wave do.
+      u32x4 pf[NB][RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float top = s[0][rt][0];
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][rt][i]);
+        const bool none = m[rt] == -INFINITY;
+        if (__ballot(top > (none ? -INFINITY : p.slack))) {
+          const float most = groups_max(top);
+          const float up = none ? (most == -INFINITY ? 0.f : most) : most > p.slack ? most : 0.f;
+          const float keep = none ? 0.f : __builtin_amdgcn_exp2f(-up * p.c);
+          m[rt] = none ? most : m[rt] + up;
+          z[rt] *= keep;
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt) o[dt][rt] *= keep;
+#pragma unroll
+          for (int t = 0; t < NK; ++t) s[t][rt] -= up;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < NK; ++t) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][i], p.c, Weights<DT>::kUp));
+            sum += e[i];
+          }
+          pf[t / 2][rt][(t & 1) * 2] = pack2<DT>(e[0], e[1]);
+          pf[t / 2][rt][(t & 1) * 2 + 1] = pack2<DT>(e[2], e[3]);
+        }
+        z[rt] += sum;
+      }
+
+      auto value_operand = [&](int n) {
+        // chunks 2 dt and 2 dt + 1 of the row, 8 bytes a lane
+        const u32x4* row = tile + value_row + n / ND * 32 * NC + value_chunk<DP>(vrow, n % ND * 2 + ((lane & 3) >> 1));
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row) + (lane & 1)));
+        const s16x4 hi =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(reinterpret_cast<const s16x4*>(row + 16 * NC) + (lane & 1)));
+        return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      // A value that is no finite number would reach the rows that do not see it as 0 times it.
+      bool odd = false;
+      if (edge) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int n = 0; n < NB * ND; ++n) most = largest_exponents<DT>(value_operand(n), most);
+        constexpr uint32_t top = DT == TF_DT_F16 ? 0x7C00u : 0x7F80u;
+        odd = __ballot((most & 0xFFFFu) >= top || most >> 16 >= top) != 0;
+      }
+      if (!odd) {
+        u32x4 vf[kRing];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) vf[n] = value_operand(n);
+#pragma unroll
+        for (int n = 0; n < NB * ND; ++n) {
+          if (n + kAhead < NB * ND) vf[(n + kAhead) % kRing] = value_operand(n + kAhead);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) o[n % ND][rt] = mfma<DT>(vf[n % kRing], pf[n / ND][rt], o[n % ND][rt]);
+          keep_order();
+        }
+      } else {
+        // Such values count as zeros in the product, and are added to the rows that see them.
+#pragma unroll
+        for (int n = 0; n < NB * ND; ++n) {
+          u32x4 v = value_operand(n);
+          drop_nonfinite<DT>(v);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) o[n % ND][rt] = mfma<DT>(v, pf[n / ND][rt], o[n % ND][rt]);
+        }
+        for (int j = max(at, from); j < min(at + KT, to); ++j) {
+          const T* row = vb + (int64_t)j * a.v_stride[0] + lg * 4;
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt) {
+            if (dt * 16 >= a.head_dim) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = Elem<DT>::load(row[dt * 16 + i]), add = fabsf(v) < INFINITY ? 0.f : v;
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) {
+                const bool seen = begin[rt] != kNowhere && begin[rt] <= j && j <= row0 + rt * 16 + (lane & 15);
+                o[dt][rt][i] += seen ? add : 0.f;
+              }
+            }
+          }
+        }
+      }
+    }
+    half ^= 1;
+  }
+
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float sum = groups_sum(z[rt]), inv = 1.f / sum;
+    if (begin[rt] == kNowhere) continue;
+    const int i = row0 + rt * 16 + (lane & 15);
+    T* out = static_cast<T*>(a.out) + i * a.out_stride[0] + head * a.out_stride[1] + lg * 4;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt)
+      if (dt * 16 < a.head_dim) {
+        const f32x4 v = sum == 0.f ? f32x4(0.f) : o[dt][rt] * inv;
+        *reinterpret_cast<u32x2*>(out + dt * 16) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+      }
+  }
+}
+
+namespace {
+
+int rows_of(int dim) { return 16 * (dim <= 128 ? 2 : 1) * kPromptWaves; }
+
+int64_t workgroups_of(const tf_exl3_prompt_attention_args& a) {
+  return ((int64_t)a.tokens + rows_of(a.head_dim) - 1) / rows_of(a.head_dim) * a.q_heads;
+}
+
+template <int DT>
+void launch(const tf_exl3_prompt_attention_args& a, const PromptPlan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)workgroups_of(a)), threads(kPromptThreads);
+  if (a.head_dim <= 64)
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, 64, 2, 64>), grid, threads, 0, stream, a, p);
+  else if (a.head_dim <= 128)
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, 128, 2, 64>), grid, threads, 0, stream, a, p);
+  else
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, 256, 1, 32>), grid, threads, 0, stream, a, p);
+}
+
+}  // namespace
+
+bool prompt_attention_fits(const tf_exl3_prompt_attention_args& a) { return launchable(workgroups_of(a), kPromptThreads); }
+
+hipError_t launch_prompt_attention(const tf_exl3_prompt_attention_args& a, hipStream_t stream) {
+  PromptPlan p;
+  p.tiles = (a.tokens + rows_of(a.head_dim) - 1) / rows_of(a.head_dim);
+  p.spread = a.q_heads % kXCDs == 0 ? a.q_heads / kXCDs : 0;
+  p.by_heads = fast_div(p.spread ? p.spread : a.q_heads), p.by_group = fast_div(a.q_heads / a.kv_heads);
+  // A scale of 0 keeps masked scores apart from others: the smallest factor does the same to sums.
+  const float c = fabsf(a.scale) * 1.4426950408889634f;
+  p.c = c > 1.2e-38f ? c : 1.2e-38f;
+  const float slack = a.dtype == TF_DT_F16 ? Weights<TF_DT_F16>::kSlack : Weights<TF_DT_BF16>::kSlack;
+  p.slack = fminf(slack / p.c, 3e38f);
+  p.negate = a.scale < 0.f;
+  if (a.dtype == TF_DT_F16)
+    launch<TF_DT_F16>(a, p, stream);
+  else
+    launch<TF_DT_BF16>(a, p, stream);
+  return hipGetLastError();
+}
+
+}  // namespace tf_exl3

@@ -32,17 +32,13 @@
 // independent workgroups of half the size measured 3 to 10% slower.
 #include <math.h>
 
-#include "ops_device.hpp"
+#include <type_traits>
+
+#include "attention_device.hpp"
 #include "ops_launch.hpp"
+#include "q4_device.hpp"
 
 namespace tf_exl3 {
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // Where a sequence begins in the line, and how many tiles each of its groups has there,
 // behind `start` places that stand for what it costs to begin one.
@@ -85,42 +81,6 @@ __device__ __forceinline__ ArgPtr arguments() {
 
 __device__ __forceinline__ FastDiv copy(DivPtr d) { return {d->m, d->shift}; }
 
-template <int DT>
-__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (DT == TF_DT_F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
-// Matrix products and reads of shared memory stay on their side; other work may cross.
-__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x2 | 0x4 | 0x10); }
-
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (DT == TF_DT_F16) {
-    const half2_t h = {(_Float16)lo, (_Float16)hi};
-    return __builtin_bit_cast(uint32_t, h);
-  } else {
-    const f32x2 f = {lo, hi};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
-  }
-}
-
-// The four lane groups' values of a row (lanes l, l + 16, l + 32, l + 48), joined.
-__device__ __forceinline__ float groups_max(float v) {
-  u32x2 s = __builtin_amdgcn_permlane16_swap(f32_to_bits(v), f32_to_bits(v), false, false);
-  v = fmaxf(bits_to_f32(s[0]), bits_to_f32(s[1]));
-  s = __builtin_amdgcn_permlane32_swap(f32_to_bits(v), f32_to_bits(v), false, false);
-  return fmaxf(bits_to_f32(s[0]), bits_to_f32(s[1]));
-}
-__device__ __forceinline__ float groups_sum(float v) {
-  u32x2 s = __builtin_amdgcn_permlane16_swap(f32_to_bits(v), f32_to_bits(v), false, false);
-  v = bits_to_f32(s[0]) + bits_to_f32(s[1]);
-  s = __builtin_amdgcn_permlane32_swap(f32_to_bits(v), f32_to_bits(v), false, false);
-  return bits_to_f32(s[0]) + bits_to_f32(s[1]);
-}
-
 __device__ __forceinline__ int cached(ArgPtr x, int b) {
   const int64_t room = (int64_t)x->a.table_pages * x->a.page_size;
   const int64_t len = x->a.lengths[b];
@@ -132,16 +92,6 @@ __device__ __forceinline__ int64_t divide(int64_t n, int64_t d) {
   if (((n | d) >> 32) == 0) return (uint32_t)n / (uint32_t)d;
   return n / d;
 }
-
-// A row's weights for the second product are 2^(x - base + kUp), its base at most kSlack below its
-// largest score so far. bf16 has fp32's exponents. fp16 begins at 2^-14 and ends at 2^16: a base that stands
-// for 2^13 keeps half a unit in the last place down to 2^-27 of the row's largest weight, and 2^-38 of that below
-// (half a step of the subnormals). Slacks of 2^8, 2^4, 2^3, 2^2 and 1 with the room used up, fp16, us: 64-node trees
-// 65.7 / 65.5 / 66.0 / 67.4 / 71.9, 32 x 16 nodes over 16384 positions 394 to 396 for all.
-template <int DT>
-struct Weights {
-  static constexpr float kUp = DT == TF_DT_F16 ? 13.f : 0.f, kSlack = DT == TF_DT_F16 ? 2.f : 8.f;
-};
 
 // A value that all lanes have, in a scalar register.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -216,29 +166,6 @@ __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
   }
 }
 
-// Shared memory holds rows of DP elements in 16-byte chunks; chunk c of row r stands at
-// c ^ (a function of r), so that neither the 16 rows x 16 bytes that a matrix operand of keys
-// takes at once nor the 8 rows x 32 bytes of a transposing load meet in a bank.
-template <int DP>
-__device__ __forceinline__ int key_chunk(int r, int c) { return c ^ (DP == 64 ? (r >> 1) & 7 : r & 15); }
-template <int DP>
-__device__ __forceinline__ int value_chunk(int r, int c) { return c ^ (DP == 64 ? ((r >> 1) & 3) << 1 : (r & 7) << 1); }
-
-// Four neighbouring columns' worth of 16-bit infinities and NaN to zero; whether any was.
-template <int DT>
-__device__ __forceinline__ bool drop_nonfinite(u32x4& v) {
-  constexpr uint32_t top = DT == TF_DT_F16 ? 0x7C00u : 0x7F80u;
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t u = v[i];
-    if ((u & top) == top) u &= 0xFFFF0000u, any = true;
-    if ((u & top << 16) == top << 16) u &= 0xFFFFu, any = true;
-    v[i] = u;
-  }
-  return any;
-}
-
 // Bits 0 .. 3: whether a row of mask `seen` sees the positions that begin `node` behind the
 // cache's end (before it where negative), `left` before the run's.
 __device__ __forceinline__ uint32_t seen_of(uint64_t seen, int node, int left) {
@@ -249,11 +176,17 @@ __device__ __forceinline__ uint32_t seen_of(uint64_t seen, int node, int left) {
 
 // S: tiles whose keys and values are on their way to registers. BUF: tiles in shared memory;
 // with two of them a tile is put there while the one before is still in use.
-template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int BUF, int WAVES>
+// Q4: the cache is in 4 bits. A thread takes groups of 32 numbers, 16 bytes of codes and their pair, which
+// become four chunks of 16-bit elements on their way from registers into shared memory; rows of the tree's
+// own nodes are loaded as they are put there.
+template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int BUF, int WAVES, bool Q4>
 __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(AttnArgs) {
   typedef uint16_t T;
   constexpr int kThreads = RG * KG * 64, KT = KG * KW, NC = DP / 8, NK = KW / 16, NB = KW / 32, ND = DP / 16, NQ = DP / 32;
-  constexpr int kStep = kThreads / NC, kLoads = KT / kStep;  // rows between a thread's loads, and how many
+  // A thread's columns of the tile, the threads of keys or values, rows between a thread's loads, and how many.
+  // In 4 bits more threads than groups of a tile share keys and values out.
+  constexpr int kColumns = Q4 ? DP / kQ4Group : NC, kSplit = Q4 && kThreads >= 2 * KT * kColumns;
+  constexpr int kLoaders = kSplit ? KT * kColumns : kThreads, kStep = kLoaders / kColumns, kLoads = KT / kStep;
   static_assert(KT % kStep == 0 && KW % 32 == 0, "");
   constexpr int kTile = KT * NC;
   constexpr int kJoin = KG > 1 ? (KG - 1) * RG * ND * 64 : 0;  // other key groups' outputs, one row tile at a time
@@ -312,17 +245,21 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
     }
 
     // The loader's part: chunk `chunk` of rows tid / NC, + kStep, ...
-    const int chunk = tid % NC, lrow = tid / NC;
+    const int chunk = tid % kColumns, lrow = (kSplit ? tid % kLoaders : tid) / kColumns;
+    const int side = kSplit ? tid / kLoaders : 0;  // of keys (0) or values, where a thread takes one of them
     x = arguments();
     const float scale_c = x->p.c, slack = x->p.slack;
-    const bool have = chunk * 8 < x->a.head_dim;
-    const T* kc = static_cast<const T*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * 8;
-    const T* vc = static_cast<const T*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * 8;
+    const bool have = chunk * (Q4 ? kQ4Group : 8) < x->a.head_dim && side < 2;
+    // In bytes where the cache is in 4 bits.
+    typedef std::conditional_t<Q4, uint8_t, T> C;
+    const C* kc = static_cast<const C*>(x->a.k_cache) + g * x->a.k_cache_stride[2] + chunk * (Q4 ? 16 : 8);
+    const C* vc = static_cast<const C*>(x->a.v_cache) + g * x->a.v_cache_stride[2] + chunk * (Q4 ? 16 : 8);
     const uint32_t page_bytes = x->p.page_bytes, slot_bytes = x->p.slot_bytes;  // page_bytes 0: wide or different strides
     const int32_t* table = x->a.table + b * x->a.table_stride;
     const int pages = x->a.pages, page_size = x->a.page_size;
     const int step_cols = x->p.step_cols, step_slots = x->p.step_slots;
     u32x4 kr[S][kLoads], vr[S][kLoads];
+    uint32_t kp[S][kLoads], vp[S][kLoads];  // scales and minima
     // A row's page and slot go on by a tile at a time; rows behind the cache's end look at its
     // last page, which is there, and are not used.
     int page[kLoads] = {}, col[kLoads], slot[kLoads];
@@ -349,7 +286,27 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         slot[i] -= wrap ? page_size : 0, col[i] += wrap;
       }
     };
-    auto load = [&](int at, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads]) {
+    const int pairs = Q4 ? x->a.head_dim / 2 - chunk * 12 : 0;  // from a group's codes to its pair
+    auto load = [&](int at, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads], uint32_t (&kp)[kLoads], uint32_t (&vp)[kLoads]) {
+      if constexpr (Q4) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const uint32_t pg = (uint32_t)page[i] < (uint32_t)pages ? page[i] : 0;
+          const C *k, *v;
+          if (page_bytes) {
+            const uint64_t off = (uint64_t)pg * page_bytes + (uint64_t)(uint32_t)slot[i] * slot_bytes;
+            k = kc + off, v = vc + off;
+          } else {
+            const ArgPtr y = arguments();
+            k = kc + pg * y->a.k_cache_stride[0] + slot[i] * y->a.k_cache_stride[1];
+            v = vc + pg * y->a.v_cache_stride[0] + slot[i] * y->a.v_cache_stride[1];
+          }
+          if (kSplit && side == 1) k = v;
+          kr[i] = *reinterpret_cast<const u32x4_word*>(k), kp[i] = *reinterpret_cast<const uint32_t*>(k + pairs);
+          if (!kSplit) vr[i] = *reinterpret_cast<const u32x4_word*>(v), vp[i] = *reinterpret_cast<const uint32_t*>(v + pairs);
+        }
+        return;
+      } else {
       const bool edge = at + KT > min(len, stop);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -375,6 +332,7 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         kr[i] = *reinterpret_cast<const u32x4*>(kp);
         vr[i] = *reinterpret_cast<const u32x4*>(vp);
       }
+      }
     };
 
     f32x4 o[ND][RT];
@@ -390,8 +348,44 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
     const int value_row = kTile + (kg * KW + vrow) * NC;
 
     // A tile from its registers into shared memory, and the registers' next one on its way.
-    auto put = [&](int at, u32x4* to, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads]) {
+    auto put = [&](int at, u32x4* to, u32x4 (&kr)[kLoads], u32x4 (&vr)[kLoads], uint32_t (&kp)[kLoads], uint32_t (&vp)[kLoads]) {
       if (!have) return;
+      if constexpr (Q4) {
+        auto put_codes = [&](int r, bool value, u32x4 codes, uint32_t pair) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int c = chunk * 4 + w;
+            const uint32_t word = codes[w];
+            to[(value ? kTile : 0) + r * NC + (value ? value_chunk<DP>(r, c) : key_chunk<DP>(r, c))] = q4_piece<DT>(word, pair);
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          put_codes(lrow + i * kStep, side == 1, kr[i], kp[i]);
+          if (!kSplit) put_codes(lrow + i * kStep, true, vr[i], vp[i]);
+        }
+        if (at + KT > min(len, stop)) {
+          // The nodes' own rows over what lies behind the cache's end there, and zeros behind the run's end.
+#pragma unroll 1
+          for (int i = 0; i < kLoads * (kSplit ? 1 : 2); ++i) {
+            const int r = lrow + (kSplit ? i : i >> 1) * kStep, node = at + r - len;
+            const bool value = kSplit ? side == 1 : i & 1;
+            if (node < 0) continue;
+            const ArgPtr y = arguments();
+            const T* row =
+                value ? static_cast<const T*>(y->a.v) + b * y->a.v_stride[0] + node * y->a.v_stride[1] + g * y->a.v_stride[2]
+                      : static_cast<const T*>(y->a.k) + b * y->a.k_stride[0] + node * y->a.k_stride[1] + g * y->a.k_stride[2];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int c = chunk * 4 + w;
+              u32x4 e = u32x4(0u);
+              if (at + r < stop) e = *reinterpret_cast<const u32x4*>(row + c * 8);
+              if (value && drop_nonfinite<DT>(e)) odd_values = 1;  // as below
+              to[(value ? kTile : 0) + r * NC + (value ? value_chunk<DP>(r, c) : key_chunk<DP>(r, c))] = e;
+            }
+          }
+        }
+      } else {
       if (at + KT > min(len, stop)) {
         // A node's values that are no numbers would reach the rows that do not see it as 0 times
         // them; they are put back below.
@@ -408,8 +402,9 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         to[r * NC + key_chunk<DP>(r, chunk)] = kr[i];
         to[kTile + r * NC + value_chunk<DP>(r, chunk)] = vr[i];
       }
+      }
       if (at + S * KT < stop) {
-        load(at + S * KT, kr, vr);
+        load(at + S * KT, kr, vr, kp, vp);
         advance();
         look_up();
       }
@@ -418,24 +413,25 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
       look_up();
 #pragma unroll
       for (int st = 0; st < S; ++st) {
-        if (begin + st * KT < stop) load(begin + st * KT, kr[st], vr[st]);
+        if (begin + st * KT < stop) load(begin + st * KT, kr[st], vr[st], kp[st], vp[st]);
         advance();
         look_up();
       }
-    } else {
+    } else if (side < 2) {
       // Columns behind the head's are zero throughout.
+      constexpr int kChunks = NC / kColumns;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = lrow + i * kStep;
+      for (int i = 0; i < kLoads * kChunks; ++i) {
+        const int r = lrow + i / kChunks * kStep, c = chunk * kChunks + i % kChunks;
 #pragma unroll
         for (int n = 0; n < BUF; ++n) {
-          lds[2 * n * kTile + r * NC + key_chunk<DP>(r, chunk)] = u32x4(0u);
-          lds[(2 * n + 1) * kTile + r * NC + value_chunk<DP>(r, chunk)] = u32x4(0u);
+          if (!kSplit || side == 0) lds[2 * n * kTile + r * NC + key_chunk<DP>(r, c)] = u32x4(0u);
+          if (!kSplit || side == 1) lds[(2 * n + 1) * kTile + r * NC + value_chunk<DP>(r, c)] = u32x4(0u);
         }
       }
     }
     __syncthreads();
-    put(begin, lds, kr[0], vr[0]);
+    put(begin, lds, kr[0], vr[0], kp[0], vp[0]);
     int half = 0;  // of shared memory, with the tile in use
     for (int at0 = begin; at0 < stop; at0 += S * KT) {
 #pragma unroll
@@ -549,7 +545,7 @@ __global__ __launch_bounds__(RG * KG * 64, WAVES) void tree_attention_kernel(Att
         if (at + KT < stop) {
           if (BUF == 1) __syncthreads();
           half = BUF == 1 ? 0 : 2 * kTile - half;
-          put(at + KT, lds + half, kr[(st + 1) % S], vr[(st + 1) % S]);
+          put(at + KT, lds + half, kr[(st + 1) % S], vr[(st + 1) % S], kp[(st + 1) % S], vp[(st + 1) % S]);
         }
       }
     }
@@ -742,7 +738,7 @@ struct Shape {
   int rows() const { return 16 * rt * rg; }
 };
 
-Shape shape_of(int dim, int rows) {
+Shape shape_of(int dim, int rows, bool q4) {
   const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   // (A wave of one row group holds 32 positions at 256 columns in half its registers.)
   if (rows <= 16 && dp < 256) return {dp, 1, 1, 2, 32, 4};
@@ -750,7 +746,8 @@ Shape shape_of(int dim, int rows) {
   if (dp == 256) return {dp, 1, 4, 1, 32, 1};
   if (rows <= 64) return {dp, 1, 4, 2, 32, 1};
   const int two = (rows + 127) / 128 * 2, three = (rows + 191) / 192 * 3;  // row tiles of 64 that are computed
-  return {dp, two < three ? 2 : 3, 4, 2, 32, 1};
+  // (Three row tiles leave no registers for codes.)
+  return {dp, two < three || q4 ? 2 : 3, 4, 2, 32, 1};
 }
 
 constexpr int kCUs = 256;
@@ -761,10 +758,10 @@ struct Layout {
   size_t seq_bytes, stat_bytes, part_bytes;
 };
 
-Layout layout_of(const tf_exl3_tree_attention_args& a) {
+Layout layout_of(const tf_exl3_tree_attention_args& a, bool q4) {
   Layout l;
   const int group = a.q_heads / a.kv_heads, rows = a.nodes * group;
-  l.s = shape_of(a.head_dim, rows);
+  l.s = shape_of(a.head_dim, rows, q4);
   AttnPlan& p = l.p;
   p.rows = rows, p.group = group;
   p.row_tiles = (rows + l.s.rows() - 1) / l.s.rows();
@@ -789,10 +786,10 @@ Layout layout_of(const tf_exl3_tree_attention_args& a) {
   return l;
 }
 
-template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int BUF, int WAVES>
+template <int DT, int DP, int RT, int RG, int KG, int KW, int S, int BUF, int WAVES, bool Q4>
 void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t stream) {
   const unsigned grid = p.workgroups ? (unsigned)p.workgroups : (unsigned)a.batch * (unsigned)p.groups;
-  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW, S, BUF, WAVES>), dim3(grid), dim3(RG * KG * 64), 0, stream,
+  hipLaunchKernelGGL((tree_attention_kernel<DT, DP, RT, RG, KG, KW, S, BUF, WAVES, Q4>), dim3(grid), dim3(RG * KG * 64), 0, stream,
                      AttnArgs{a, p});
   if (p.workgroups == 0) return;
   const int rows = a.kv_heads * p.rows, tile_rows = 16 * RT * RG;
@@ -805,47 +802,48 @@ void launch(const tf_exl3_tree_attention_args& a, const AttnPlan& p, hipStream_t
                        AttnArgs{a, p}, by_tile, tile_rows);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, bool Q4>
 void launch_dim(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream_t stream) {
   const Shape& s = l.s;
   if constexpr (DP < 256) {
-    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32, 1, 1, 2>(a, l.p, stream);
-    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 2, 2, 2>(a, l.p, stream);
-    if (s.rt == 1) return launch<DT, DP, 1, 4, 2, 32, 3, 2, 2>(a, l.p, stream);
-    if (s.rt == 2) return launch<DT, DP, 2, 4, 2, 32, 1, 2, 2>(a, l.p, stream);
-    return launch<DT, DP, 3, 4, 2, 32, 1, 1, 2>(a, l.p, stream);
+    if (s.rg == 1) return launch<DT, DP, 1, 1, 2, 32, 1, 1, 2, Q4>(a, l.p, stream);
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 2, 2, 2, Q4>(a, l.p, stream);
+    if (s.rt == 1) return launch<DT, DP, 1, 4, 2, 32, 3, 2, 2, Q4>(a, l.p, stream);
+    if (Q4 || s.rt == 2) return launch<DT, DP, 2, 4, 2, 32, 1, 2, 2, Q4>(a, l.p, stream);
+    if constexpr (!Q4) return launch<DT, DP, 3, 4, 2, 32, 1, 1, 2, Q4>(a, l.p, stream);
   } else {
-    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 1, 1>(a, l.p, stream);
-    return launch<DT, DP, 1, 4, 1, 32, 1, 2, 1>(a, l.p, stream);
+    if (s.rg == 2) return launch<DT, DP, 1, 2, 2, 32, 1, 1, 1, Q4>(a, l.p, stream);
+    return launch<DT, DP, 1, 4, 1, 32, 1, 2, 1, Q4>(a, l.p, stream);
   }
 }
 
-template <int DT>
+template <int DT, bool Q4>
 void launch_type(const tf_exl3_tree_attention_args& a, const Layout& l, hipStream_t stream) {
   if (l.s.dp == 64)
-    launch_dim<DT, 64>(a, l, stream);
+    launch_dim<DT, 64, Q4>(a, l, stream);
   else if (l.s.dp == 128)
-    launch_dim<DT, 128>(a, l, stream);
+    launch_dim<DT, 128, Q4>(a, l, stream);
   else
-    launch_dim<DT, 256>(a, l, stream);
+    launch_dim<DT, 256, Q4>(a, l, stream);
 }
 
 }  // namespace
 
-size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a) {
-  const Layout l = layout_of(a);
+static size_t workspace(const tf_exl3_tree_attention_args& a, bool q4) {
+  const Layout l = layout_of(a, q4);
   return l.seq_bytes + l.stat_bytes + l.part_bytes + 16;
 }
 
 // The second launch has a workgroup for no more than each of 64 * 65535 rows, the first with pieces no more
 // of them than the chip holds.
-bool tree_attention_fits(const tf_exl3_tree_attention_args& a) {
-  const Layout l = layout_of(a);
+static bool fits(const tf_exl3_tree_attention_args& a, bool q4) {
+  const Layout l = layout_of(a, q4);
   return launchable((int64_t)a.batch * l.p.groups, l.s.rg * l.s.kg * 64) || l.p.workgroups > 0;
 }
 
-hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream) {
-  Layout l = layout_of(a);
+template <bool Q4>
+static hipError_t launch_call(const tf_exl3_tree_attention_args& a, hipStream_t stream) {
+  Layout l = layout_of(a, Q4);
   char* ws = static_cast<char*>(a.workspace);
   l.p.seq = reinterpret_cast<SeqTiles*>(ws);
   l.p.stat = reinterpret_cast<float2*>(ws + l.seq_bytes);
@@ -856,18 +854,27 @@ hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream
   const float slack = a.dtype == TF_DT_F16 ? Weights<TF_DT_F16>::kSlack : Weights<TF_DT_BF16>::kSlack;
   l.p.slack = fminf(slack / l.p.c, 3e38f);
   l.p.negate = a.scale < 0.f;
-  const int64_t page = a.k_cache_stride[0] * 2, slot = a.k_cache_stride[1] * 2;
-  const bool same = a.v_cache_stride[0] * 2 == page && a.v_cache_stride[1] * 2 == slot;
+  constexpr int kBytes = Q4 ? 1 : 2;  // that the caches' strides count
+  const int64_t page = a.k_cache_stride[0] * kBytes, slot = a.k_cache_stride[1] * kBytes;
+  const bool same = a.v_cache_stride[0] * kBytes == page && a.v_cache_stride[1] * kBytes == slot;
   l.p.page_bytes = same && page < (1ll << 32) && slot < (1ll << 32) ? (uint32_t)page : 0;
   l.p.slot_bytes = (uint32_t)slot;
   l.p.step_cols = l.s.tile() / a.page_size, l.p.step_slots = l.s.tile() % a.page_size;
   l.p.by_group = fast_div(l.p.group), l.p.by_page = fast_div(a.page_size);
   l.p.by_row_tiles = fast_div(l.p.row_tiles), l.p.by_rows = fast_div(l.p.rows), l.p.by_groups = fast_div(l.p.groups);
   if (a.dtype == TF_DT_F16)
-    launch_type<TF_DT_F16>(a, l, stream);
+    launch_type<TF_DT_F16, Q4>(a, l, stream);
   else
-    launch_type<TF_DT_BF16>(a, l, stream);
+    launch_type<TF_DT_BF16, Q4>(a, l, stream);
   return hipGetLastError();
 }
+
+size_t tree_attention_workspace(const tf_exl3_tree_attention_args& a) { return workspace(a, false); }
+bool tree_attention_fits(const tf_exl3_tree_attention_args& a) { return fits(a, false); }
+hipError_t launch_tree_attention(const tf_exl3_tree_attention_args& a, hipStream_t stream) { return launch_call<false>(a, stream); }
+
+size_t tree_attention_q4_workspace(const tf_exl3_tree_attention_args& a) { return workspace(a, true); }
+bool tree_attention_q4_fits(const tf_exl3_tree_attention_args& a) { return fits(a, true); }
+hipError_t launch_tree_attention_q4(const tf_exl3_tree_attention_args& a, hipStream_t stream) { return launch_call<true>(a, stream); }
 
 }  // namespace tf_exl3
