@@ -592,7 +592,8 @@ int tf_exl3_cache_read_q4(const tf_exl3_cache_read_q4_args* a, void* stream);
 /*
  * tree_attention_q4: tree_attention whose cache is in 4 bits; the nodes' own k and v are
  * of dtype, as q. A cached key or value is what cache_read_q4 gives in that type. head_dim is
- * a multiple of 32 up to 256, k_cache_stride and v_cache_stride are in bytes.
+ * a multiple of 32 up to 256, k_cache_stride and v_cache_stride are in bytes, those over pages
+ * and slots below 2^32.
  */
 int tf_exl3_tree_attention_q4(const tf_exl3_tree_attention_args* a, void* stream);
 size_t tf_exl3_tree_attention_q4_workspace(const tf_exl3_tree_attention_args* a);

@@ -22,31 +22,34 @@ __device__ __forceinline__ Q4Pair q4_unpack(uint32_t pair) {
   return {f16_bits_to_f32((uint16_t)pair), f16_bits_to_f32((uint16_t)(pair >> 16))};
 }
 
-// The values of a word's eight codes in fp32. A pair of codes is a pair of fp16 subnormals, code * 2^-24, which the mixed multiply-add
-// takes as they are; the scale makes up for it (its products with codes are exact in fp32).
+// The values of a word's eight codes in fp32. A pair of codes, masked where it stands, is a pair of fp16
+// subnormals, code * 2^-24 or, 4 bits up, code * 2^-20, which the mixed multiply-add takes as they are;
+// the scales make up for it (their products with codes are exact in fp32).
 __device__ __forceinline__ void q4_values(uint32_t word, Q4Pair p, float (&x)[8]) {
-  const float scale = p.scale * 16777216.f;
+  const float scales[2] = {p.scale * 16777216.f, p.scale * 1048576.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t t = (word >> 4 * i) & 0x000F000Fu;
+    const uint32_t t = (i < 2 ? word : word >> 8) & (i % 2 ? 0x00F000F0u : 0x000F000Fu);
     const half2_t h = __builtin_bit_cast(half2_t, t);
-    x[2 * i] = __builtin_fmaf((float)h[0], scale, p.low);
-    x[2 * i + 1] = __builtin_fmaf((float)h[1], scale, p.low);
+    x[2 * i] = __builtin_fmaf((float)h[0], scales[i % 2], p.low);
+    x[2 * i + 1] = __builtin_fmaf((float)h[1], scales[i % 2], p.low);
   }
 }
 
-// Eight values as a 16-byte piece of a row of DT. fp16: 1024 + code in the last bits of an fp16,
-// less 1024, times the scale plus the minimum with one rounding.
+// Eight values as a 16-byte piece of a row of DT. fp16: the codes in the last bits of 1024 or, 4 bits up,
+// of 64, less that, times the scale plus the minimum with one rounding.
 template <int DT>
 __device__ __forceinline__ u32x4 q4_piece(uint32_t word, uint32_t pair) {
   u32x4 v;
   if constexpr (DT == TF_DT_F16) {
     const half2_t h = __builtin_bit_cast(half2_t, pair);
-    const half2_t scale = {h[0], h[0]}, low = {h[1], h[1]}, base = {(_Float16)1024, (_Float16)1024};
+    const half2_t scale = {h[0], h[0]}, low = {h[1], h[1]};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t t = ((word >> 4 * i) & 0x000F000Fu) | 0x64006400u;
-      v[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(half2_t, t) - base, scale, low));
+      const uint32_t bits = (i < 2 ? word : word >> 8) & (i % 2 ? 0x00F000F0u : 0x000F000Fu);
+      const uint32_t base = i % 2 ? 0x54005400u : 0x64006400u;
+      const half2_t n = __builtin_bit_cast(half2_t, bits | base) - __builtin_bit_cast(half2_t, base);
+      v[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(n, scale, low));
     }
   } else {
     float x[8];
