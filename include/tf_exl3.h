@@ -507,8 +507,9 @@ int tf_exl3_norm_rotate(const tf_exl3_norm_rotate_args* a, void* stream);
  * Numerics as in tree_attention. Rows of out in front of offsets[0] and from
  * offsets[batch] on are left as they were, whatever q, k and v hold there. Offsets are
  * taken within [0, tokens]; where they do not ascend, rows are not as stated, but no
- * address leaves its buffer. The same call gives the same bits; a row's do not depend on
- * other sequences but through where its own begins within a tile of tokens.
+ * address leaves its buffer. The same call gives the same bits. The order of a row's fp32
+ * sums goes by the number of tokens and heads and by which rows share its tile of 64 or 128 tokens;
+ * values elsewhere have no say.
  *
  *   dtype     TF_DT_F16 or TF_DT_BF16
  *   head_dim  a multiple of 16, up to 256; q_heads a multiple of kv_heads

@@ -82,6 +82,41 @@ def test_packed_batches(gpu, lengths, front, behind):
     run(len(lengths), "bf16", lengths, 4, 2, 128, front=front, behind=behind)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [48, 64, 96, 128])
+@pytest.mark.parametrize("lengths", [[400], [1, 130, 0, 200, 69], [3] * 20 + [64, 33, 128, 115]])
+def test_two_row_tiles(gpu, dt, dim, lengths):
+    """So many heads that a wave takes two row tiles; a few of them are looked at."""
+    say(f"two row tiles {dt} {dim} {lengths[:5]}")
+    hq, hkv, front, behind = 352, 176, 2, 5
+    offsets = np.cumsum([front, *lengths]).tolist()
+    qkv = rows_of(dim, dt, offsets[-1] + behind, hq, hkv, dim)
+    qkv[offsets[-1]:] = float("nan")
+    out = torch.full((qkv.shape[0], hq, dim), 7.0, dtype=DT[dt], device="cuda")
+    tq.prompt_attention(*qkv.cuda().split([hq, hkv, hkv], dim=1), torch.tensor(offsets, dtype=torch.int32, device="cuda"), out=out)
+    for h in (0, 3, 175, 350):
+        some = qkv[:, [h, hq + h // 2, hq + hkv + h // 2]]
+        check(out[:, [h]], some, [1, 1, 1], offsets, dt, None, 7.0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_odd_values_under_two_row_tiles(gpu, dt, dim):
+    """Infinities among the values: rows that do not see them keep their bits, others get them."""
+    hq, n = 352, 400
+    offsets = torch.tensor([0, 150, n], dtype=torch.int32, device="cuda")
+    qkv = rows_of(dim + 1, dt, n, hq, hq, dim).cuda()
+    clean = tq.prompt_attention(*qkv.split([hq] * 3, dim=1), offsets)
+    qkv[100, 2 * hq + 7, 3] = float("inf")
+    qkv[390, 2 * hq + 7, 5] = -float("inf")
+    out = tq.prompt_attention(*qkv.split([hq] * 3, dim=1), offsets)
+    changed = torch.zeros((n, hq, dim), dtype=torch.bool, device="cuda")
+    changed[100:150, 7, 3] = True
+    changed[390:, 7, 5] = True
+    assert torch.equal(out[~changed], clean[~changed])
+    assert (out[100:150, 7, 3] == float("inf")).all() and (out[390:, 7, 5] == -float("inf")).all()
+
+
 def test_many_sequences(gpu):
     """More of them than a wave has lanes, some empty."""
     run(4, "f16", [(7 * b) % 11 for b in range(300)], 2, 1, 64)

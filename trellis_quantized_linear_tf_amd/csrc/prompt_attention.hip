@@ -9,6 +9,12 @@
 // Products are transposed as in tree attention: S^T = K Q^T leaves a lane with 4 positions of one row
 // per tile of 16, and its weights are where O^T = V^T P^T wants them. Only tiles that some row of a wave does
 // not see as a whole are masked.
+//
+// One prompt of 16384 tokens, 32 heads over 8 of 128, bf16: 2.2 TFLOP in 2.00 ms, 1.10 PFLOP/s, where torch's product of
+// 8192^3 reached 1.21 on the same card: matrix products and vector instructions (150 a wave and 64 keys, 32 of them
+// exponentials) fill it between them. Steps of 32 keys whose weights are made between the products of the next step's
+// scores measured 2.11 ms. 24 prompts of 512 to 2050 tokens, fp16: 560 us, 660 TFLOP/s; a tenth of the products each are
+// the diagonal's and those of tiles with two sequences' rows, the rest starts and the last workgroups.
 #include <math.h>
 
 #include "attention_device.hpp"
@@ -29,16 +35,30 @@ constexpr int kXCDs = 8;
 constexpr int kNowhere = 0x7FFFFFFF;  // the beginning of a row that belongs to no sequence
 
 // Where the sequence of token i begins; kNowhere in front of the first and behind the last one.
-__device__ __forceinline__ int sequence_begin(const int32_t* offsets, int batch, int i) {
-  int lo = -1, hi = batch + 1;  // offsets[lo] <= i < offsets[hi], as if there were such ends
+// `sample` is a lane's entry of the wave's 64 evenly spread offsets, `every` entries apart: with 63 sequences or
+// fewer they are all of them, and nothing else is loaded.
+__device__ __forceinline__ int sequence_begin(const int32_t* offsets, int batch, int i, int sample, int every) {
+  int lo = -1, hi = batch / every + 1;  // samples: that of lo is at most i, that of hi more, as if there were such ends
+  for (int width = hi - lo; width > 1; width = (width + 1) / 2) {  // as often for every lane
+    const int mid = lo + (hi - lo) / 2, v = __builtin_amdgcn_ds_bpermute(max(mid, 0) * 4, sample);
+    if (hi - lo > 1) {
+      if (v <= i)
+        lo = mid;
+      else
+        hi = mid;
+    }
+  }
+  int begin = __builtin_amdgcn_ds_bpermute(max(lo, 0) * 4, sample);
+  if (lo < 0) return kNowhere;
+  lo *= every, hi = min(hi * every, batch + 1);
   while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (offsets[mid] <= i)
-      lo = mid;
+    const int mid = lo + (hi - lo) / 2, v = offsets[mid];
+    if (v <= i)
+      lo = mid, begin = v;
     else
       hi = mid;
   }
-  return lo < 0 || lo == batch ? kNowhere : max(offsets[lo], 0);
+  return lo == batch ? kNowhere : max(begin, 0);
 }
 
 template <typename F>
@@ -97,22 +117,8 @@ __global__ __launch_bounds__(kPromptThreads, 2) void prompt_attention_kernel(tf_
   const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row0 = tile * kRows + wave * 16 * RT;  // the wave's first token
 
-  // Rows, the beginnings of their sequences, and what the wave and the workgroup look at.
-  int begin[RT];
-  int low = kNowhere, high = 0, latest = 0;  // first key, past the last, latest beginning
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int i = row0 + rt * 16 + (lane & 15);
-    begin[rt] = i < a.tokens ? sequence_begin(a.offsets, a.batch, i) : kNowhere;
-    if (begin[rt] > i) begin[rt] = kNowhere;
-    low = min(low, begin[rt]), latest = max(latest, begin[rt]);
-    if (begin[rt] != kNowhere) high = max(high, i + 1);
-  }
-  low = __builtin_amdgcn_readfirstlane(rows_reduce(low, [](int x, int y) { return min(x, y); }));
-  high = __builtin_amdgcn_readfirstlane(rows_reduce(high, [](int x, int y) { return max(x, y); }));
-  latest = __builtin_amdgcn_readfirstlane(rows_reduce(latest, [](int x, int y) { return max(x, y); }));
-  if (lane == 0) ranges[0][wave] = low, ranges[1][wave] = high;
-
+  const int every = a.batch / 64 + 1;
+  const int sample = a.offsets[min(lane * every, a.batch)];
   u32x4 q[RT][NQ];
   {
     const uint32_t flip = p.negate ? 0x80008000u : 0u;
@@ -124,11 +130,27 @@ __global__ __launch_bounds__(kPromptThreads, 2) void prompt_attention_kernel(tf_
       for (int n = 0; n < NQ; ++n) {
         const int d = n * 32 + lg * 8;
         q[rt][n] = u32x4(0u);
-        if (begin[rt] != kNowhere && d < a.head_dim) q[rt][n] = *reinterpret_cast<const u32x4*>(row + d);
+        if (i < a.tokens && d < a.head_dim) q[rt][n] = *reinterpret_cast<const u32x4*>(row + d);
         q[rt][n] ^= flip;
       }
     }
   }
+  // Rows, the beginnings of their sequences, and what the wave and the workgroup look at.
+  int begin[RT];
+  int low = kNowhere, high = 0, latest = 0;  // first key, past the last, latest beginning
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int i = row0 + rt * 16 + (lane & 15);
+    begin[rt] = sequence_begin(a.offsets, a.batch, i, sample, every);
+    if (i >= a.tokens || begin[rt] > i) begin[rt] = kNowhere;
+    low = min(low, begin[rt]), latest = max(latest, begin[rt]);
+    if (begin[rt] != kNowhere) high = max(high, i + 1);
+  }
+  low = __builtin_amdgcn_readfirstlane(rows_reduce(low, [](int x, int y) { return min(x, y); }));
+  high = __builtin_amdgcn_readfirstlane(rows_reduce(high, [](int x, int y) { return max(x, y); }));
+  latest = __builtin_amdgcn_readfirstlane(rows_reduce(latest, [](int x, int y) { return max(x, y); }));
+  if (lane == 0) ranges[0][wave] = low, ranges[1][wave] = high;
+
   // Columns behind the head's are zero throughout.
   if (a.head_dim < DP) {
     for (int i = tid; i < 4 * kTile; i += kPromptThreads) lds[i] = u32x4(0u);
@@ -153,26 +175,16 @@ __global__ __launch_bounds__(kPromptThreads, 2) void prompt_attention_kernel(tf_
   for (int n = 0; n < kKinds; ++n) kc[n] = key_chunk<DP>(lrow + n * kStep, chunk);
   const int vc = value_chunk<DP>(lrow, chunk);
   auto stage = [&](int at, int buffer) {
-    const T* const kt = kb + (int64_t)at * a.k_stride[0];
-    const T* const vt = vb + (int64_t)at * a.v_stride[0];
     const uint32_t dst = place + buffer * 2 * kTile * 16;
-    const int last = a.tokens - 1 - at;
-    if (last >= KT - 1) {
+    const char* const kt = reinterpret_cast<const char*>(kb) + (uint64_t)(uint32_t)at * ks;
+    const char* const vt = reinterpret_cast<const char*>(vb) + (uint64_t)(uint32_t)at * vs;
+    const uint32_t last = min(a.tokens - 1 - at, KT);  // behind the last token its row again
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const int c = kc[n % kKinds];
-        if (c * 8 < a.head_dim)
-          load_to_shared(kt + (int64_t)n * kStep * a.k_stride[0], lrow * ks + c * 16, dst + n * kPromptThreads * 16);
-        if (vc * 8 < a.head_dim)
-          load_to_shared(vt + (int64_t)n * kStep * a.v_stride[0], lrow * vs + vc * 16, dst + (kTile + n * kPromptThreads) * 16);
-      }
-    } else {  // behind the last token its row again
-#pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const int c = kc[n % kKinds], row = min(lrow + n * kStep, last);
-        if (c * 8 < a.head_dim) load_to_shared(kt, row * ks + c * 16, dst + n * kPromptThreads * 16);
-        if (vc * 8 < a.head_dim) load_to_shared(vt, row * vs + vc * 16, dst + (kTile + n * kPromptThreads) * 16);
-      }
+    for (int n = 0; n < kLoads; ++n) {
+      const int c = kc[n % kKinds];
+      const uint32_t k = min(lrow * ks + (uint32_t)(n * kStep) * ks, last * ks), v = min(lrow * vs + (uint32_t)(n * kStep) * vs, last * vs);
+      if (c * 8 < a.head_dim) load_to_shared(kt, k + c * 16, dst + n * kPromptThreads * 16);
+      if (vc * 8 < a.head_dim) load_to_shared(vt, v + vc * 16, dst + (kTile + n * kPromptThreads) * 16);
     }
   };
 
@@ -344,30 +356,45 @@ __global__ __launch_bounds__(kPromptThreads, 2) void prompt_attention_kernel(tf_
 
 namespace {
 
-int rows_of(int dim) { return 16 * (dim <= 128 ? 2 : 1) * kPromptWaves; }
+// Row tiles of a wave: two, but one at 256 columns, whose outputs fill the registers, and where workgroups of 128 tokens
+// would be so few (three a CU, four at 64 columns) that the longest is waited for. One against two, us on the
+// GPU: 8 prompts of 2048 tokens, 32 heads over 8 of 128, 4096 workgroups 364 / 300; 4 of 1000, 1024 workgroups 73 / 68
+// (at 64 columns 2 of 2000 59 / 71); one of 2050, 544 workgroups 59 / 75; one of 300, 96 workgroups 11.7 / 14.7; one of 77
+// 6.7 / 8.4.
+int row_tiles_of(const tf_exl3_prompt_attention_args& a) {
+  const int64_t two = ((int64_t)a.tokens + 32 * kPromptWaves - 1) / (32 * kPromptWaves) * a.q_heads;
+  return a.head_dim > 128 || two <= (a.head_dim <= 64 ? 1024 : 768) ? 1 : 2;
+}
 
-int64_t workgroups_of(const tf_exl3_prompt_attention_args& a) {
-  return ((int64_t)a.tokens + rows_of(a.head_dim) - 1) / rows_of(a.head_dim) * a.q_heads;
+int64_t tiles_of(const tf_exl3_prompt_attention_args& a) {
+  const int rows = 16 * row_tiles_of(a) * kPromptWaves;
+  return ((int64_t)a.tokens + rows - 1) / rows;
+}
+
+template <int DT, int DP, int RT, int KT>
+void launch_rows(const tf_exl3_prompt_attention_args& a, const PromptPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((prompt_attention_kernel<DT, DP, RT, KT>), dim3((unsigned)(tiles_of(a) * a.q_heads)), dim3(kPromptThreads), 0,
+                     stream, a, p);
 }
 
 template <int DT>
 void launch(const tf_exl3_prompt_attention_args& a, const PromptPlan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)workgroups_of(a)), threads(kPromptThreads);
+  const bool one = row_tiles_of(a) == 1;
   if (a.head_dim <= 64)
-    hipLaunchKernelGGL((prompt_attention_kernel<DT, 64, 2, 64>), grid, threads, 0, stream, a, p);
+    one ? launch_rows<DT, 64, 1, 64>(a, p, stream) : launch_rows<DT, 64, 2, 64>(a, p, stream);
   else if (a.head_dim <= 128)
-    hipLaunchKernelGGL((prompt_attention_kernel<DT, 128, 2, 64>), grid, threads, 0, stream, a, p);
+    one ? launch_rows<DT, 128, 1, 64>(a, p, stream) : launch_rows<DT, 128, 2, 64>(a, p, stream);
   else
-    hipLaunchKernelGGL((prompt_attention_kernel<DT, 256, 1, 32>), grid, threads, 0, stream, a, p);
+    launch_rows<DT, 256, 1, 32>(a, p, stream);
 }
 
 }  // namespace
 
-bool prompt_attention_fits(const tf_exl3_prompt_attention_args& a) { return launchable(workgroups_of(a), kPromptThreads); }
+bool prompt_attention_fits(const tf_exl3_prompt_attention_args& a) { return launchable(tiles_of(a) * a.q_heads, kPromptThreads); }
 
 hipError_t launch_prompt_attention(const tf_exl3_prompt_attention_args& a, hipStream_t stream) {
   PromptPlan p;
-  p.tiles = (a.tokens + rows_of(a.head_dim) - 1) / rows_of(a.head_dim);
+  p.tiles = (int)tiles_of(a);
   p.spread = a.q_heads % kXCDs == 0 ? a.q_heads / kXCDs : 0;
   p.by_heads = fast_div(p.spread ? p.spread : a.q_heads), p.by_group = fast_div(a.q_heads / a.kv_heads);
   // A scale of 0 keeps masked scores apart from others: the smallest factor does the same to sums.
