@@ -473,7 +473,7 @@ size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k);
  *
  *   dtype        of q, k and the outputs; weight_dtype of q_weight and k_weight (each
  *                [head_dim] or NULL: all ones); any of the three
- *   q, k         [batch][tokens][heads][head_dim], strides [batch, token, head]
+ *   q, k         [batch][tokens][heads][head_dim], strides [batch, token, head], below 2^32
  *   q_out, k_out likewise; each may be its input itself (the same pointer and strides), else
  *                they overlap no input; rows of q and k may alternate in one buffer
  *   positions    int32 [batch][tokens], rows positions_stride apart

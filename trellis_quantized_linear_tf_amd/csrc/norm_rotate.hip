@@ -4,7 +4,8 @@
 // same for every head of a token: the threads work them out once, in 64 bits up to the part of a turn,
 // and leave them in shared memory. Then LANES lanes take a row, two pieces of 8 elements each, chosen
 // so that both elements of every pair are in one lane: the squares' sum is LANES - 1 register moves, the
-// rotation none. Bound by the rows' bytes, read once and written once.
+// rotation none. Bound by the rows' bytes, read once and written once: a row is on its way while the one before is
+// worked at, the first of them while the angles are.
 #include <math.h>
 
 #include "ops_device.hpp"
@@ -18,8 +19,26 @@ constexpr int kMostTokens = 8;  // of a workgroup
 
 struct RotatePlan {
   int tokens;  // of a workgroup
-  FastDiv by_rows, by_tokens, by_angles;
+  int parts;   // workgroups that share its rows
+  FastDiv by_q_heads, by_kv_heads, by_tokens, by_angles;
 };
+
+// Two pieces of eight elements of a row, as they lie there.
+template <int DT>
+struct RawRow {
+  static constexpr int kPieces = DT == TF_DT_F32 ? 2 : 1;
+  u32x4 x[kPieces], y[kPieces];
+};
+
+template <int DT>
+__device__ __forceinline__ void numbers(const u32x4 (&raw)[RawRow<DT>::kPieces], float (&x)[8]) {
+  if constexpr (DT == TF_DT_F32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = bits_to_f32(raw[i / 4][i % 4]);
+  } else {
+    Elem<DT>::unpack(raw[0], x);
+  }
+}
 
 __device__ __forceinline__ void load_weights(const void* w, int dtype, int at, float (&x)[8]) {
   if (dtype == TF_DT_F32)
@@ -47,6 +66,53 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
   __shared__ float cosines[kTurns], sines[kTurns];
   const int all = a.batch * a.tokens, first = blockIdx.x * p.tokens;
   const int here = min(p.tokens, all - first), angles = a.rotary_dim / 2;
+  const int u = threadIdx.x % LANES;
+  const bool have = u < a.head_dim / 16;  // the others add zeros to the sum
+  const bool turned = u < a.rotary_dim / 16;
+  const bool halves = turned && !a.interleaved;
+  const int at0 = halves ? 8 * u : 16 * u, at1 = halves ? angles + 8 * u : 16 * u + 8;
+
+  // Rows in this order: the tokens' queries, then their keys.
+  struct Place {
+    const T* in;
+    T* out;
+    int token;  // of the workgroup's
+    bool query;
+  };
+  const int queries = here * a.q_heads, rows = queries + here * a.kv_heads;
+  auto place = [&](int r) {
+    Place x;
+    x.query = r < queries;
+    const int row = x.query ? r : r - queries;
+    x.token = (x.query ? p.by_q_heads : p.by_kv_heads).div(row);
+    const int head = row - x.token * (x.query ? a.q_heads : a.kv_heads);
+    const int t = first + x.token, b = p.by_tokens.div(t), i = t - b * a.tokens;
+    const int64_t* si = x.query ? a.q_stride : a.k_stride;
+    const int64_t* so = x.query ? a.q_out_stride : a.k_out_stride;
+    auto offset = [&](const int64_t* s) {  // below 2^32 each
+      return (uint64_t)(uint32_t)b * (uint32_t)s[0] + (uint64_t)(uint32_t)i * (uint32_t)s[1] + (uint64_t)(uint32_t)head * (uint32_t)s[2];
+    };
+    x.in = static_cast<const T*>(x.query ? a.q : a.k) + offset(si);
+    x.out = static_cast<T*>(x.query ? a.q_out : a.k_out) + offset(so);
+    return x;
+  };
+  auto load = [&](const Place& x, RawRow<DT>& raw) {
+#pragma unroll
+    for (int n = 0; n < RawRow<DT>::kPieces; ++n) {
+      raw.x[n] = raw.y[n] = u32x4(0u);
+      if (have) raw.x[n] = load_piece(x.in + at0 + 4 * n), raw.y[n] = load_piece(x.in + at1 + 4 * n);
+    }
+  };
+
+  constexpr int kSlots = kRotateThreads / LANES;
+  const int step = kSlots * p.parts;
+  int r = blockIdx.y * kSlots + threadIdx.x / LANES;
+  Place now = {};
+  RawRow<DT> raw = {};
+  if (r < rows) {
+    now = place(r);
+    load(now, raw);
+  }
   for (int i = threadIdx.x; i < here * angles; i += kRotateThreads) {
     const int j = p.by_angles.div(i), t = first + j, b = p.by_tokens.div(t);
     const double pos = a.positions[b * a.positions_stride + (t - b * a.tokens)];
@@ -57,45 +123,41 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
     cosines[i] = c, sines[i] = s;
   }
   __syncthreads();
-  const int u = threadIdx.x % LANES, rotated = a.rotary_dim / 16;
-  const bool have = u < a.head_dim / 16;  // the others add zeros to the sum
-  const bool turned = u < rotated;
-  const bool halves = turned && !a.interleaved;
-  const int at0 = halves ? 8 * u : 16 * u, at1 = halves ? angles + 8 * u : 16 * u + 8;
-  const int heads = a.q_heads + a.kv_heads;
-  for (int r = threadIdx.x / LANES; r < here * heads; r += kRotateThreads / LANES) {
-    const int j = p.by_rows.div(r), t = first + j, b = p.by_tokens.div(t), i = t - b * a.tokens;
-    const int row = r - j * heads;
-    const bool query = row < a.q_heads;
-    const int head = query ? row : row - a.q_heads;
-    const int64_t* si = query ? a.q_stride : a.k_stride;
-    const int64_t* so = query ? a.q_out_stride : a.k_out_stride;
-    const T* in = static_cast<const T*>(query ? a.q : a.k) + b * si[0] + i * si[1] + head * si[2];
-    T* out = static_cast<T*>(query ? a.q_out : a.k_out) + b * so[0] + i * so[1] + head * so[2];
-    float x[8] = {}, y[8] = {};
-    if (have) {
-      load8<DT>(in + at0, x);
-      load8<DT>(in + at1, y);
+
+  float w0[8], w1[8];
+  int weights_of = -1;  // keys (0) or queries
+  while (r < rows) {
+    const int ahead = r + step;
+    Place next = {};
+    RawRow<DT> raw_next = {};
+    if (ahead < rows) {
+      next = place(ahead);
+      load(next, raw_next);
     }
+    float x[8], y[8];
+    numbers<DT>(raw.x, x);
+    numbers<DT>(raw.y, y);
     if (a.norm) {
+      if (weights_of != (int)now.query) {
+        weights_of = now.query;
+        const void* w = now.query ? a.q_weight : a.k_weight;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) w0[n] = w1[n] = 1.f;
+        if (w && have) {
+          load_weights(w, a.weight_dtype, at0, w0);
+          load_weights(w, a.weight_dtype, at1, w1);
+        }
+      }
       float squares = 0.f;
 #pragma unroll
       for (int n = 0; n < 8; ++n) squares = __builtin_fmaf(x[n], x[n], __builtin_fmaf(y[n], y[n], squares));
       squares = lanes_sum<LANES>(squares);
       const float scale = 1.f / sqrtf(squares / (float)a.head_dim + a.eps);
-      const void* w = query ? a.q_weight : a.k_weight;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) x[n] *= scale, y[n] *= scale;
-      if (w && have) {
-        float w0[8], w1[8];
-        load_weights(w, a.weight_dtype, at0, w0);
-        load_weights(w, a.weight_dtype, at1, w1);
-#pragma unroll
-        for (int n = 0; n < 8; ++n) x[n] *= w0[n], y[n] *= w1[n];
-      }
+      for (int n = 0; n < 8; ++n) x[n] = x[n] * scale * w0[n], y[n] = y[n] * scale * w1[n];
     }
     if (turned) {
-      const float *c = cosines + j * angles + 8 * u, *s = sines + j * angles + 8 * u;
+      const float *c = cosines + now.token * angles + 8 * u, *s = sines + now.token * angles + 8 * u;
       if (a.interleaved) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -113,34 +175,44 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
       }
     }
     if (have) {
-      store8<DT>(out + at0, x);
-      store8<DT>(out + at1, y);
+      store8<DT>(now.out + at0, x);
+      store8<DT>(now.out + at1, y);
     }
+    r = ahead, now = next, raw = raw_next;
   }
 }
 
-static RotatePlan plan_of(const tf_exl3_norm_rotate_args& a) {
+static RotatePlan plan_of(const tf_exl3_norm_rotate_args& a, int slots) {
   const int angles = a.rotary_dim / 2 > 0 ? a.rotary_dim / 2 : 1;
   RotatePlan p;
-  const int64_t share = (int64_t)a.batch * a.tokens / 1024;  // tokens of one of 1024 workgroups
+  const int64_t all = (int64_t)a.batch * a.tokens, share = all / 1024;  // tokens of one of 1024 workgroups
   const int most = kTurns / angles < kMostTokens ? kTurns / angles : kMostTokens;
   p.tokens = share < 1 ? 1 : share < most ? (int)share : most;
-  p.by_rows = fast_div(a.q_heads + a.kv_heads), p.by_tokens = fast_div(a.tokens), p.by_angles = fast_div(angles);
+  // Few tokens: their rows are shared out, as far as each thread still has one.
+  const int rows = (a.q_heads + a.kv_heads + slots - 1) / slots;
+  p.parts = all >= 512 ? 1 : rows;
+  p.by_q_heads = fast_div(a.q_heads), p.by_kv_heads = fast_div(a.kv_heads);
+  p.by_tokens = fast_div(a.tokens), p.by_angles = fast_div(angles);
   return p;
+}
+
+template <int DT, int LANES>
+static void launch(const tf_exl3_norm_rotate_args& a, hipStream_t stream) {
+  const RotatePlan p = plan_of(a, kRotateThreads / LANES);
+  hipLaunchKernelGGL((norm_rotate_kernel<DT, LANES>), dim3((unsigned)(((int64_t)a.batch * a.tokens + p.tokens - 1) / p.tokens), p.parts),
+                     dim3(kRotateThreads), 0, stream, a, p);
 }
 
 template <int DT>
 static void launch(const tf_exl3_norm_rotate_args& a, hipStream_t stream) {
-  const RotatePlan p = plan_of(a);
-  const dim3 grid((unsigned)(((int64_t)a.batch * a.tokens + p.tokens - 1) / p.tokens)), threads(kRotateThreads);
   if (a.head_dim <= 64)
-    hipLaunchKernelGGL((norm_rotate_kernel<DT, 4>), grid, threads, 0, stream, a, p);
+    launch<DT, 4>(a, stream);
   else if (a.head_dim <= 128)
-    hipLaunchKernelGGL((norm_rotate_kernel<DT, 8>), grid, threads, 0, stream, a, p);
+    launch<DT, 8>(a, stream);
   else if (a.head_dim <= 256)
-    hipLaunchKernelGGL((norm_rotate_kernel<DT, 16>), grid, threads, 0, stream, a, p);
+    launch<DT, 16>(a, stream);
   else
-    hipLaunchKernelGGL((norm_rotate_kernel<DT, 32>), grid, threads, 0, stream, a, p);
+    launch<DT, 32>(a, stream);
 }
 
 hipError_t launch_norm_rotate(const tf_exl3_norm_rotate_args& a, hipStream_t stream) {

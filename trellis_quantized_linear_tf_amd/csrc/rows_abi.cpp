@@ -83,6 +83,10 @@ int tf_exl3_norm_rotate(const tf_exl3_norm_rotate_args* args, void* stream) {
       !strides_ok(a->k_out_stride, 1) || !apart(a->batch, a->tokens, a->q_heads, a->q_out_stride) ||
       !apart(a->batch, a->tokens, a->kv_heads, a->k_out_stride))
     return TF_E_SIZE;
+  for (int i = 0; i < 3; ++i)
+    if (a->q_stride[i] >= (1ll << 32) || a->k_stride[i] >= (1ll << 32) || a->q_out_stride[i] >= (1ll << 32) ||
+        a->k_out_stride[i] >= (1ll << 32))
+      return TF_E_SIZE;
   if (a->batch == 0 || a->tokens == 0) return TF_OK;
   if (!a->q || !a->k || !a->q_out || !a->k_out || (a->rotary_dim > 0 && (!a->positions || !a->frequencies))) return TF_E_NULL;
   const size_t e = elem_size(a->dtype), we = elem_size(a->weight_dtype);
