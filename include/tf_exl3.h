@@ -532,7 +532,7 @@ int tf_exl3_prompt_attention(const tf_exl3_prompt_attention_args* a, void* strea
 /*
  * A cache in 4 bits. A row of head_dim numbers x is kept in groups of 32:
  *
- *   x as fp32, NaN as 0, within [-65504, 65504]
+ *   x as fp32, NaN as 0, within [-65408, 65408] (so that no value is an infinity of fp16)
  *   m = RN16(min x) (never -0),  s = RN16(RN32((max x - min x) / 15))
  *   n[i] = rint(RN32(RN32(x[i] - m) / s)) within 0 .. 15 (ties to even), 0 where s is 0
  *

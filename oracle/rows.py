@@ -56,7 +56,7 @@ def q4_codes(x):
     """(codes uint8 [..., dim], scale and low fp16 [..., dim / 32]) of rows of numbers, step by step in fp32."""
     x = np.asarray(x, dtype=np.float32)
     x = np.where(np.isnan(x), np.float32(0), x)
-    x = np.clip(x, np.float32(-65504), np.float32(65504)).reshape(*x.shape[:-1], -1, GROUP)
+    x = np.clip(x, np.float32(-65408), np.float32(65408)).reshape(*x.shape[:-1], -1, GROUP)
     low, high = x.min(-1), x.max(-1)
     scale = ((high - low) / np.float32(15)).astype(np.float16)
     low = low.astype(np.float16) + np.float16(0)  # no -0

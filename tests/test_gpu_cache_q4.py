@@ -79,6 +79,18 @@ def test_numbers_next_to_borders_and_none(gpu, dt):
     append(k, v, cache, table, lengths, False)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_the_largest_numbers(gpu, dt):
+    """fp16's largest numbers of both signs in a group: their bytes, and finite values in every type."""
+    k, v, cache, table, lengths, _ = setup(14, dt, 1, 6, 1, 64, 16, [0])
+    k[..., 0], k[..., 1], v[..., 40] = 65504.0, -65504.0, 65000.0
+    k[0, 1] = k[0, 1].sign() * 65504.0
+    caches = append(k, v, cache, table, lengths, False)
+    for to in DT:
+        for got in tq.cache_read_q4(*caches, table.cuda(), (lengths + 6).cuda(), 6, dtype=DT[to]):
+            assert torch.isfinite(got).all()
+
+
 def test_nodes_and_counts(gpu):
     k, v, cache, table, lengths, _ = setup(5, "bf16", 4, 6, 2, 64, 16, [0, 5, 17, 30])
     nodes = torch.tensor([[0, 2, 5, -1, -1, -1], [3, -1, 4, 9, 0, 1], [0, 1, 2, 3, 4, 5], [5, 5, 5, 5, 5, 5]], dtype=torch.int32)

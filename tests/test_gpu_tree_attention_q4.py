@@ -63,6 +63,53 @@ def test_every_head_size_and_row_tile(gpu, dt, dim, rows):
     check(case, run(case))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("nodes,hq", [(9, 4), (16, 4), (12, 6), (16, 8), (33, 2), (50, 8), (64, 4)])
+def test_many_rows_of_long_tables(gpu, dt, dim, nodes, hq):
+    """Tables with so much room that a wave takes two or four row tiles, with short and empty sequences in them."""
+    say(f"long tables {dt} {dim} {nodes} {hq}")
+    case = Case4(dim + nodes, dt, [97, 0, 700, 131], nodes, hq, 2, dim, 64, heads_first=dim % 64 == 0, room=800)
+    check(case, run(case))
+
+
+@pytest.mark.parametrize("dt,dim,nodes", [("bf16", 128, 16), ("f16", 64, 20), ("bf16", 64, 8), ("f16", 128, 40), ("bf16", 256, 9)])
+def test_many_rows_of_many_sequences(gpu, dt, dim, nodes):
+    """Groups that one workgroup takes as a whole, with two or four row tiles."""
+    say(f"many sequences {dt} {dim} {nodes}")
+    case = Case4(dim, dt, [(37 * b) % 300 for b in range(260)], nodes, 8, 2, dim, 16, room=64)
+    got = run(case)
+    some = [0, 1, 7, 130, 259]
+    for name in ("q", "k", "v", "mask", "table", "lengths"):
+        setattr(case, name, getattr(case, name)[some])
+    check(case, got[some])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_long_sequences_of_many_rows(gpu, dt, dim):
+    """Pieces that begin and end within a sequence, with two or four row tiles."""
+    say(f"long, many rows {dt} {dim}")
+    case = Case4(dim + 1, dt, [5001, 1, 2500, 300], 16, 8, 2, dim, 64, room=900)
+    check(case, run(case))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("nodes", [16, 40])
+def test_nodes_that_some_of_many_rows_see(gpu, bad, nodes):
+    masks = [[1 << min(i, nodes - 2) for i in range(nodes)]] * 2
+    case = Case4(6, "bf16", [30, 64], nodes, 4, 2, 128, 64, masks=masks, room=2000)
+    want = run(case)
+    case.k[:, nodes - 1], case.v[:, nodes - 1] = bad, bad
+    assert torch.equal(run(case), want)
+    case.v[:, 3, 1, 7] = float("inf")
+    got = run(case)
+    assert (got[:, 3, 2:, 7] == float("inf")).all()
+    rest = torch.ones_like(got, dtype=torch.bool)
+    rest[:, 3, 2:, 7] = False
+    assert torch.equal(got[rest], want[rest])
+
+
 @pytest.mark.parametrize("page", [1, 3, 16, 24, 32, 64, 100, 256])
 @pytest.mark.parametrize("heads_first", [False, True])
 def test_every_page(gpu, page, heads_first):

@@ -23,7 +23,7 @@ def test_ties_go_to_even():
     assert list(rows.q4_codes(x)[0][:5]) == [15, 0, 2, 2, 4]
 
 
-@pytest.mark.parametrize("value", [0.0, -7.25, 65504.0, 1e-7])
+@pytest.mark.parametrize("value", [0.0, -7.25, 65408.0, 1e-7])
 def test_equal_numbers_stand_for_themselves(value):
     """Code and scale of 0, the minimum in fp16."""
     x = np.full(64, value, np.float32)
@@ -36,8 +36,15 @@ def test_numbers_that_are_none():
     x = np.linspace(-1, 1, 32).astype(np.float32)
     x[3], x[4], x[5] = np.nan, np.inf, -np.inf
     codes, scale, low = rows.q4_codes(x)
-    assert low[0] == -65504 and scale[0] == np.float16(np.float32(131008) / 15)
+    assert low[0] == -65408 and scale[0] == np.float16(np.float32(130816) / 15)
     assert codes[4] == 15 and codes[5] == 0 and codes[3] in (7, 8)
+
+
+@pytest.mark.parametrize("low", [-65504.0, -65408.0, -3e4, 0.0, 65000.0])
+def test_the_largest_numbers_stay_finite_in_fp16(low):
+    for high in (65504.0, 65408.0, 65376.0, 64000.0, 3e38):
+        x = np.linspace(low, high, 32).astype(np.float32)
+        assert np.isfinite(rows.round_to(rows.q4_unpack(rows.q4_pack(x)), "f16")).all()
 
 
 def test_bytes_of_a_row():

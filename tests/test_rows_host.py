@@ -164,7 +164,7 @@ def rotate_args(**bad):
     (dict(batch=1 << 12, tokens=1 << 12), -10), (dict(q_heads=0), -10), (dict(kv_heads=0), -10), (dict(q_heads=65536), -10),
     (dict(head_dim=8), -10), (dict(head_dim=72), -10), (dict(head_dim=528), -10), (dict(rotary_dim=8), -10),
     (dict(rotary_dim=80), -10), (dict(rotary_dim=-16), -10), (dict(eps=-1.0), -10), (dict(eps=float("nan")), -10),
-    (dict(q_stride=(-1, 1, 1)), -10), (dict(q_out_stride=(0, 256, 64)), -10), (dict(positions_stride=-1), -10),
+    (dict(q_stride=(-1, 1, 1)), -10), (dict(k_stride=(1 << 32, 128, 64)), -10), (dict(q_out_stride=(0, 256, 64)), -10), (dict(positions_stride=-1), -10),
     (dict(q=None), -5), (dict(k_out=None), -5), (dict(positions=None), -5), (dict(frequencies=None), -5),
     (dict(q=FAKE + 1), -6), (dict(positions=FAKE + 4 * STEP + 2), -6), (dict(q_weight=FAKE + 2 * STEP + 1), -6),
     (dict(q_out=FAKE + 128), -7), (dict(q_out=FAKE, q_out_stride=(768, 256, 32)), -7), (dict(q_out=FAKE + STEP), -7),
@@ -251,7 +251,7 @@ def test_library_refuses_read(lib, bad, code):  # noqa: F811
 
 @pytest.mark.parametrize("bad,code", [
     (dict(head_dim=80), -10), (dict(head_dim=48), -10), (dict(dtype=0), -4), (dict(nodes=65), -10), (dict(k_cache=FAKE + 4 * STEP + 2), -6),
-    (dict(v_cache_stride=(1280, 80, 42)), -10), (dict(out=FAKE + 4 * STEP), -7), (dict(workspace_bytes=0), -11), (dict(q=None), -5),
+    (dict(v_cache_stride=(1280, 80, 42)), -10), (dict(k_cache_stride=(1 << 32, 80, 40)), -10), (dict(out=FAKE + 4 * STEP), -7), (dict(workspace_bytes=0), -11), (dict(q=None), -5),
     (dict(batch=0, q=None), 0),
 ])
 def test_library_refuses_attention(lib, bad, code):  # noqa: F811
@@ -266,7 +266,7 @@ def test_library_refuses_attention(lib, bad, code):  # noqa: F811
     fill(a, bad)
     assert lib.tf_exl3_tree_attention_q4(a, None) == code
     assert lib.tf_exl3_tree_attention_q4(None, None) == -5
-    assert (lib.tf_exl3_tree_attention_q4_workspace(a) > 0) == (code not in (-10, -4) or "v_cache_stride" in bad)
+    assert (lib.tf_exl3_tree_attention_q4_workspace(a) > 0) == (code not in (-10, -4) or "v_cache_stride" in bad or "k_cache_stride" in bad)
 
 
 def test_argument_structures_have_the_headers_layout(tmp_path):

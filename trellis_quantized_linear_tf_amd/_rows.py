@@ -70,10 +70,17 @@ def _check_norm_rotate(q, k, positions, frequencies, q_weight, k_weight, outs):
     _one_gpu(q, k, positions if frequencies is not None else None, frequencies, q_weight, k_weight, *outs)
 
 
-def _steps(t):
-    """Strides of [batch, token, head] of rows [batch][tokens][heads][dim] or [tokens][heads][dim]."""
-    s = t.stride()
-    return s[:3] if len(s) == 4 else (0, s[0], s[1])
+def _is_weight(torch, w, dtype, dim, device):
+    return (
+        (dtype is torch.bfloat16 or dtype is torch.float16 or dtype is torch.float32) and w.dtype is dtype
+        and w.shape == (dim,) and w.is_contiguous() and w.get_device() == device
+    )
+
+
+def _pair(out):
+    if len(out) != 2:
+        raise ValueError("out must be a pair of tensors")
+    return out
 
 
 def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None):
@@ -87,47 +94,52 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
     (positions are not looked at). q_weight, k_weight [dim], None for ones. eps None: no norm,
     and no weights. out: the pair of results, which may be (q, k) themselves."""
     torch = _torch()
-    outs = (None, None) if out is None else out
-    if len(outs) != 2:
-        raise ValueError("out must be a pair of tensors")
+    q_out, k_out = (None, None) if out is None else _pair(out)
     if eps is None and not (q_weight is None and k_weight is None):
         raise ValueError("weights belong to the norm: eps is None")
     dev = -1
     try:
-        *tokens, heads, dim = shape = q.shape
-        t, rows, d = q.dtype, k.shape, q.get_device()
-        w = q_weight if q_weight is not None else k_weight
+        shape, rows, t, d = q.shape, k.shape, q.dtype, q.get_device()
+        dim, tokens = shape[-1], shape[:-2]
+        w = k_weight if q_weight is None else q_weight
         if (
             (t is torch.bfloat16 or t is torch.float16 or t is torch.float32) and k.dtype is t
-            and (len(tokens) == 2 or len(tokens) == 1) and list(rows[:-2]) == tokens and rows[-1] == dim
+            and (len(shape) == 4 or len(shape) == 3) and rows[:-2] == tokens and rows[-1] == dim
             and q.stride(-1) == k.stride(-1) == 1 and d == k.get_device()
-            and (frequencies is None or frequencies.dtype is torch.float32 and len(frequencies.shape) == 1
-                 and frequencies.is_contiguous() and positions.dtype is torch.int32 and list(positions.shape) == tokens
+            and (frequencies is None or frequencies.dtype is torch.float32 and frequencies.dim() == 1
+                 and frequencies.is_contiguous() and positions.dtype is torch.int32 and positions.shape == tokens
                  and positions.stride(-1) == 1 and frequencies.get_device() == d == positions.get_device())
-            and (w is None or w.dtype in _floats())
-            and all(x is None or x.dtype is w.dtype and x.shape == (dim,) and x.is_contiguous() and x.get_device() == d
-                    for x in (q_weight, k_weight))
-            and all(o is None or o.dtype is t and o.shape == x.shape and o.stride(-1) == 1 and o.get_device() == d
-                    for o, x in zip(outs, (q, k)))
+            and (w is None or _is_weight(torch, w, w.dtype, dim, d) and (w is k_weight or k_weight is None
+                                                                         or _is_weight(torch, k_weight, w.dtype, dim, d)))
+            and (q_out is None or q_out.dtype is t and q_out.shape == shape and q_out.stride(-1) == 1 and q_out.get_device() == d)
+            and (k_out is None or k_out.dtype is t and k_out.shape == rows and k_out.stride(-1) == 1 and k_out.get_device() == d)
         ):
             dev = d
     except (AttributeError, IndexError, RuntimeError, TypeError, ValueError):
         pass
     if dev < 0:
-        _check_norm_rotate(q, k, positions, frequencies, q_weight, k_weight, outs)
-        *tokens, heads, dim = shape = q.shape
-        rows, w = k.shape, q_weight if q_weight is not None else k_weight
-    q_out = q.new_empty(shape) if outs[0] is None else outs[0]
-    k_out = k.new_empty(rows) if outs[1] is None else outs[1]
-    batch, count = (1, tokens[0]) if len(tokens) == 1 else tokens
-    turned = frequencies is not None
+        _check_norm_rotate(q, k, positions, frequencies, q_weight, k_weight, (q_out, k_out))
+        shape, rows = q.shape, k.shape
+        w = k_weight if q_weight is None else q_weight
+    if q_out is None:
+        q_out = q.new_empty(shape)
+    if k_out is None:
+        k_out = k.new_empty(rows)
+    code = _dt_code(q.dtype)
+    if len(shape) == 4:
+        batch, tokens, heads, dim = shape
+        steps = (*q.stride()[:3], *k.stride()[:3], *q_out.stride()[:3], *k_out.stride()[:3],
+                 0 if frequencies is None else positions.stride(0))
+    else:
+        batch, (tokens, heads, dim) = 1, shape
+        steps = (0, *q.stride()[:2], 0, *k.stride()[:2], 0, *q_out.stride()[:2], 0, *k_out.stride()[:2], 0)
+    angles = (0, 0, 0) if frequencies is None else (2 * frequencies.shape[0], positions.data_ptr(), frequencies.data_ptr())
     a = _lib.NormRotateArgs()
     _pack(
-        _ROTATE, a, _dt_code(q.dtype), _dt_code(q.dtype if w is None else w.dtype), batch, count, heads, rows[-2], dim,
-        2 * frequencies.shape[0] if turned else 0, bool(interleaved), eps is not None, 0.0 if eps is None else eps,
-        q.data_ptr(), k.data_ptr(), _ptr(q_weight) or 0, _ptr(k_weight) or 0, positions.data_ptr() if turned else 0,
-        frequencies.data_ptr() if turned else 0, q_out.data_ptr(), k_out.data_ptr(), *_steps(q), *_steps(k), *_steps(q_out),
-        *_steps(k_out), positions.stride(0) if turned and len(tokens) == 2 else 0)
+        _ROTATE, a, code, code if w is None else _dt_code(w.dtype), batch, tokens, heads, rows[-2], dim, angles[0],
+        bool(interleaved), eps is not None, 0.0 if eps is None else eps, q.data_ptr(), k.data_ptr(),
+        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), angles[1], angles[2],
+        q_out.data_ptr(), k_out.data_ptr(), *steps)
     _run(q, load().tf_exl3_norm_rotate, a)
     if _followed(q, k, q_weight, k_weight):
         return tuple(_without_gradient("norm_rotate", o, x, y) for o, x, y in ((q_out, q, q_weight), (k_out, k, k_weight)))

@@ -51,6 +51,8 @@ int tree_attention(const tf_exl3_tree_attention_args* args, bool q4, void* strea
       !strides_ok(a->k_cache_stride, q4 ? 4 : 8) || !strides_ok(a->v_cache_stride, q4 ? 4 : 8) || !strides_ok(a->out_stride, 4) ||
       !apart(a->batch, a->nodes, a->q_heads, a->out_stride))
     return TF_E_SIZE;
+  for (int i = 0; i < 2; ++i)
+    if (q4 && (a->k_cache_stride[i] >= (1ll << 32) || a->v_cache_stride[i] >= (1ll << 32))) return TF_E_SIZE;
   if (a->batch == 0) return TF_OK;
   if (!a->q || !a->k || !a->v || !a->mask || !a->k_cache || !a->v_cache || !a->lengths || !a->out || !a->workspace ||
       (a->table_pages > 0 && !a->table))

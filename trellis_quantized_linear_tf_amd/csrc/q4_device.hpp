@@ -9,7 +9,9 @@
 namespace tf_exl3 {
 
 constexpr int kQ4Group = 32;
-constexpr float kQ4Most = 65504.f;  // of a number's magnitude: fp16's largest
+// Of a number's magnitude: a scale that was rounded up takes the largest code of numbers within +-M to
+// M (1 + 2^-10), which has to stay below 65520, where fp16 rounds to infinity.
+constexpr float kQ4Most = 65408.f;
 
 typedef u32x4 u32x4_word __attribute__((aligned(4)));  // codes begin at any word
 

@@ -493,11 +493,7 @@ void launch_type(const tf_exl3_tree_attention_args& a, const Layout& l, hipStrea
 
 size_t tree_attention_q4_workspace(const tf_exl3_tree_attention_args& a) { return layout(a).workspace(); }
 
-bool tree_attention_q4_fits(const tf_exl3_tree_attention_args& a) {
-  for (int i = 0; i < 2; ++i)
-    if (a.k_cache_stride[i] >= (1ll << 32) || a.v_cache_stride[i] >= (1ll << 32)) return false;
-  return layout_fits(a, layout(a));
-}
+bool tree_attention_q4_fits(const tf_exl3_tree_attention_args& a) { return layout_fits(a, layout(a)); }
 
 hipError_t launch_tree_attention_q4(const tf_exl3_tree_attention_args& a, hipStream_t stream) {
   Layout l = layout(a);
