@@ -1,14 +1,16 @@
 """Speculative decoding with trees of drafts, a one-layer model around the trellis
 projection, on one GPU:
 
-    python examples/speculative_decode.py [--steps 24] [--batch 4] [--temperature 0.0]
+    python examples/speculative_decode.py [--steps 24] [--batch 4] [--temperature 0.0] [--cache-bits 4]
 
 Each step drafts a tree with a small drafter, runs the tree's nodes through the model at
 once (project, tree_attention), keeps the path that the model's own samples follow
 (verify_tree), puts that path's keys and values into the paged cache (cache_append), and
 teaches the drafter the model's top logits (distill). With temperature 0 the tokens are
 those of decoding one by one, but where logits tie within the order of attention's fp32 sums,
-which goes by the tree and the batch. Weights are random; the projections are 4-bit trellis streams.
+which goes by the tree and the batch. With --cache-bits 4 (cache_append_q4, tree_attention_q4)
+they may differ: a node sees the others of its tree as they are, and once they are accepted as
+the cache holds them. Weights are random; the projections are 4-bit trellis streams.
 """
 
 import argparse
@@ -71,17 +73,27 @@ class Model:
 
 
 class Cache:
-    def __init__(self, batch, room, device):
+    def __init__(self, batch, room, device, bits=16):
         per = -(-room // PAGE)
-        shape = (batch * per, PAGE, KV_HEADS, HEAD_DIM)
-        self.k, self.v = (torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
+        self.bits = bits
+        if bits == 4:  # a head's slots behind one another
+            shape = (batch * per, KV_HEADS, PAGE, tq.q4_row_bytes(HEAD_DIM))
+            self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device).transpose(1, 2) for _ in range(2))
+        else:
+            shape = (batch * per, PAGE, KV_HEADS, HEAD_DIM)
+            self.k, self.v = (torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
         g = torch.Generator().manual_seed(7)
         self.table = torch.randperm(batch * per, generator=g).view(batch, per).to(torch.int32).to(device)
         self.lengths = torch.zeros(batch, dtype=torch.int32, device=device)
 
     def append(self, k, v, nodes=None, counts=None):
-        tq.cache_append(k, v, self.k, self.v, self.table, self.lengths, nodes, counts)
+        append = tq.cache_append_q4 if self.bits == 4 else tq.cache_append
+        append(k, v, self.k, self.v, self.table, self.lengths, nodes, counts)
         self.lengths += k.shape[1] if counts is None else counts
+
+    def attend(self, q, k, v, mask):
+        attention = tq.tree_attention_q4 if self.bits == 4 else tq.tree_attention
+        return attention(q, k, v, mask, self.k, self.v, self.table, self.lengths)
 
 
 class Drafter:
@@ -108,7 +120,7 @@ class Drafter:
         return loss.mean()
 
 
-def decode(model, prompt, tokens, trees=True, temperature=0.0, drafter=None, seed=3):
+def decode(model, prompt, tokens, trees=True, temperature=0.0, drafter=None, seed=3, cache_bits=16):
     """Continues prompt [batch][length] by at least `tokens` tokens a sequence. Returns the new tokens
     (a list a sequence), the steps taken and the drafter's losses."""
     batch = prompt.shape[0]
@@ -120,7 +132,7 @@ def decode(model, prompt, tokens, trees=True, temperature=0.0, drafter=None, see
     mask = torch.tensor([seen] * batch, dtype=torch.int64, device=model.device)
     heat = torch.full((batch,), temperature, device=model.device)
     g = torch.Generator(device=model.device).manual_seed(seed)
-    cache = Cache(batch, prompt.shape[1] + (tokens + 1) * nodes, model.device)
+    cache = Cache(batch, prompt.shape[1] + (tokens + 1) * nodes, model.device, cache_bits)
     _, (_, k, v) = model.rows(prompt[:, :-1])
     cache.append(k, v)
     last = prompt[:, -1].to(torch.int32)
@@ -129,7 +141,7 @@ def decode(model, prompt, tokens, trees=True, temperature=0.0, drafter=None, see
     while min(map(len, out)) < tokens:
         drafts = drafter.draft(model, last) if trees else last[:, None].contiguous()
         x, (q, k, v) = model.rows(drafts)
-        logits = model.logits(x, tq.tree_attention(q, k, v, mask, cache.k, cache.v, cache.table, cache.lengths))
+        logits = model.logits(x, cache.attend(q, k, v, mask))
         u = torch.rand((batch, nodes), generator=g, device=model.device)
         accepted, count, last = tq.verify_tree(logits, drafts, parents, u, heat)
         cache.append(k, v, accepted, count)
@@ -146,14 +158,17 @@ def main():
     parser.add_argument("--steps", type=int, default=24, help="tokens a sequence, at least")
     parser.add_argument("--batch", type=int, default=4)
     parser.add_argument("--temperature", type=float, default=0.0)
+    parser.add_argument("--cache-bits", type=int, choices=(16, 4), default=16)
     args = parser.parse_args()
     model = Model()
     g = torch.Generator().manual_seed(5)
     prompt = torch.randint(0, VOCAB, (args.batch, 21), generator=g).to(model.device)
-    plain, plain_steps, _ = decode(model, prompt, args.steps, trees=False, temperature=args.temperature)
+    plain, plain_steps, _ = decode(model, prompt, args.steps, trees=False, temperature=args.temperature,
+                                  cache_bits=args.cache_bits)
     drafter = Drafter(model.device)
     for run in range(3):
-        got, steps, losses = decode(model, prompt, args.steps, temperature=args.temperature, drafter=drafter)
+        got, steps, losses = decode(model, prompt, args.steps, temperature=args.temperature, drafter=drafter,
+                                    cache_bits=args.cache_bits)
         same = [a[: args.steps] == b[: args.steps] for a, b in zip(got, plain)]
         print(f"run {run}: {steps} steps for {plain_steps} tokens, drafter's loss {losses[0]:.3f} -> {losses[-1]:.3f}, "
               f"as decoded one by one: {sum(same)} of {len(same)}")
