@@ -91,6 +91,24 @@ def test_the_largest_numbers(gpu, dt):
             assert torch.isfinite(got).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_every_size_of_group(gpu, dt):
+    """262144 groups of sizes and middles from 2^-40 to 2^17; one in eight has a number that is none or too large."""
+    k, v, cache, table, lengths, _ = setup(15, dt, 2, 2048, 4, 128, 64, [5, 90])
+    g = torch.Generator().manual_seed(16)
+    for x in (k, v):
+        groups = (*x.shape[:-1], x.shape[-1] // 32, 1)
+        size, middle = (2.0 ** (torch.rand(groups, generator=g) * 57 - 40) for _ in range(2))
+        middle *= torch.randint(-1, 2, groups, generator=g)
+        y = torch.randn((*groups[:-1], 32), generator=g) * size + middle
+        odd = torch.tensor([float("nan"), float("inf"), -float("inf"), 1e30, -1e30, 65450.0, -65500.0, 65408.0])
+        at = torch.randint(0, 8 * 32, groups, generator=g)
+        place = torch.arange(32) == at
+        y = torch.where(place, odd[torch.randint(0, 8, groups, generator=g)], y)
+        x.copy_(y.flatten(-2))
+    append(k, v, cache, table, lengths, False)
+
+
 def test_nodes_and_counts(gpu):
     k, v, cache, table, lengths, _ = setup(5, "bf16", 4, 6, 2, 64, 16, [0, 5, 17, 30])
     nodes = torch.tensor([[0, 2, 5, -1, -1, -1], [3, -1, 4, 9, 0, 1], [0, 1, 2, 3, 4, 5], [5, 5, 5, 5, 5, 5]], dtype=torch.int32)

@@ -3,9 +3,10 @@
 // A workgroup takes some tokens with all their heads. The angles' cosines and sines are the
 // same for every head of a token: the threads work them out once, in 64 bits up to the part of a turn,
 // and leave them in shared memory. Then LANES lanes take a row, two pieces of 8 elements each, chosen
-// so that both elements of every pair are in one lane: the squares' sum is LANES - 1 register moves, the
+// so that both elements of every pair are in one lane: the squares' sum is log2(LANES) register moves, the
 // rotation none. Bound by the rows' bytes, read once and written once: a row is on its way while the one before is
-// worked at, the first of them while the angles are.
+// worked at, the first of them while the angles are. 4 x 4099 tokens of 40 rows of 128, bf16, 336 MB: 77 us, 4.4 TB/s,
+// where a copy of 4 GiB reached 4.7 on the same card.
 #include <math.h>
 
 #include "ops_device.hpp"
@@ -187,10 +188,13 @@ static RotatePlan plan_of(const tf_exl3_norm_rotate_args& a, int slots) {
   RotatePlan p;
   const int64_t all = (int64_t)a.batch * a.tokens, share = all / 1024;  // tokens of one of 1024 workgroups
   const int most = kTurns / angles < kMostTokens ? kTurns / angles : kMostTokens;
+  // 1, 2, 4, 8 tokens a workgroup, us on the GPU, 40 rows of 128 a token: 1024 tokens 7.0 / 7.1 / 8.4 / 11.8, 2048
+  // 11.8 / 10.5 / 10.8 / 13.7, 4096 20.0 / 18.3 / 16.4 / 17.3, 16384 89 / 75 / 71 / 71.
   p.tokens = share < 1 ? 1 : share < most ? (int)share : most;
-  // Few tokens: their rows are shared out, as far as each thread still has one.
+  // Few tokens: their rows are shared out, as far as each thread still has one. One workgroup a token against that, us:
+  // 1 token 4.1 / 3.3, 512 5.2 / 4.7, 1024 7.1 / 7.8, 4096 16.5 / 17.2 (5 rows of 256 a token: the same at all of them).
   const int rows = (a.q_heads + a.kv_heads + slots - 1) / slots;
-  p.parts = all >= 512 ? 1 : rows;
+  p.parts = all > 512 ? 1 : rows;
   p.by_q_heads = fast_div(a.q_heads), p.by_kv_heads = fast_div(a.kv_heads);
   p.by_tokens = fast_div(a.tokens), p.by_angles = fast_div(angles);
   return p;
