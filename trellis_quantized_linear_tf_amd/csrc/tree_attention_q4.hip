@@ -450,16 +450,24 @@ constexpr int waves_of(int dp, int rt) { return dp == 256 || rt == 4 ? 2 : dp * 
 // Row tiles of a wave: as many as there are, up to four (two at 256 columns), as long as enough tiles are left
 // to give every workgroup that the chip holds a few: a number is made once for all of a wave's rows, but one wave alone
 // takes long over many rows. One, two, four row tiles, us on the GPU, 8 heads of 128, by places (tiles of 128
-// positions of each row tile): 32 rows, 64 places 12 / 14 / -, 1056 24 / 26 / -, 6336 52 / 41 / -; 64 rows, 128 places
-// of four row tiles 13 / 14 / 18, 504 26 / 25 / 28, 1024 31 / 30 / 32, 2048 46 / 39 / 39, 4032 58 / 47 / 44.
+// positions of each row tile): 32 rows, 64 places of two row tiles 12.8 / 14.1, 1056 23.4 / 26.7, 2112 31.9 / 29.9, 6336
+// 77 / 46; 64 rows, 128 places of four 14 / 15 / 19, 1024 32 / 29 / 33, 2176 47 / 37 / 39, 3968 90 / 57 / 46, 7936
+// 164 / 100 / 64.
 Shape shape_of(const tf_exl3_tree_attention_args& a) {
   const int dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256, rows = a.nodes * (a.q_heads / a.kv_heads);
   const int64_t tiles = ((int64_t)a.table_pages * a.page_size + a.nodes) / (4 * kQ4Positions) + 1;
   const int64_t groups = (int64_t)a.batch * a.kv_heads * tiles;
   int rt = 1;
-  if (rows > 16 && groups * ((rows + 31) / 32) >= 1024) rt = 2;
-  if (dp < 256 && rows > 32 && groups * ((rows + 63) / 64) >= 2048) rt = 4;
-  return {dp, rt, 1, 4, kQ4Positions, dp == 256 && rt == 2 ? 1 : waves_of(dp, rt)};  // (84 KB of shared memory)
+  if (rows > 16 && groups * ((rows + 31) / 32) >= 1536) rt = 2;
+  if (dp < 256 && rows > 32 && groups * ((rows + 63) / 64) >= 2560) rt = 4;
+  // Workgroups a CU that the line is cut for: what it holds (of 256 columns and two row tiles, 84 KB of shared memory,
+  // one), but two where a piece would be a few tiles: beginning and joining it takes as long. Two, three, four, us on the
+  // GPU: 1088 places 16.1 / 14.3 / 14.2, 2056 29.8 / 32.1 / 32.3, 4608 32.2 / 36.3 / 35.6, 6336 in two row tiles 46.9 /
+  // 48.9 / -, 8320 48.7 / 50.4 / 53.4, 12480 45.7 / 44.7 / 44.2, 33024 154 / 150 / 148.
+  const int64_t places = groups * ((rows + 16 * rt - 1) / (16 * rt));
+  int resident = dp == 256 && rt == 2 ? 1 : waves_of(dp, rt);
+  if (resident > 2 && places >= 2048 && places < 10240) resident = 2;
+  return {dp, rt, 1, 4, kQ4Positions, resident};
 }
 
 // The more groups there are, the longer one workgroup may take over one of them before two launches and pieces of
