@@ -471,10 +471,11 @@ Shape shape_of(const tf_exl3_tree_attention_args& a) {
 }
 
 // The more groups there are, the longer one workgroup may take over one of them before two launches and pieces of
-// equal time take less. Whole against cut, us on the GPU, rows of 128: 8 groups, 3 tiles 9.3 / 11.0, 4 tiles 10.5 /
-// 10.9, 6 tiles 13.0 / 11.2; 128 groups, 6 tiles 13.8 / 14.6 (32 rows 15.3 / 22.5), 8 tiles 16.5 / 14.8 (20.5 / 23.6);
-// 256 groups, 12 tiles 24.2 / 24.3 (28.5 / 33.3), 16 tiles 29.9 / 27.3; 512 groups, 16 tiles 34 / 36 (42 / 49), 23 tiles
-// 46 / 42 (57 / 57).
+// equal time take less. Whole against cut, us on the GPU, 8 rows of 128 (32 rows): 8 groups, 3 tiles 9.9 / 11.3 (10.2 /
+// 11.7), 4 tiles 11.3 / 11.4, 5 tiles 12.7 / 11.4 (13.0 / 11.8); 128 groups, 6 tiles 16.9 / 16.1 (19.6 / 23.8), 8 tiles
+// 20.0 / 16.6 (23.0 / 26.9), 10 tiles 23.5 / 21.1 (26.2 / 26.1); 256 groups, 10 tiles 27.2 / 27.0 (30.1 / 33.2), 12 tiles
+// 30.3 / 28.1 (32.8 / 33.8), 16 tiles 37 / 32 (41 / 36); 512 groups, 12 tiles 41 / 41 (44 / 53), 16 tiles 51 / 50 (56 /
+// 56), 23 tiles 66 / 60 (76 / 81).
 Layout layout(const tf_exl3_tree_attention_args& a) {
   const Shape s = shape_of(a);
   return layout_of(a, s, s.rt > 2 ? 2 : 1, [](int64_t groups) { return groups >= 512 ? 16 : groups >= 256 ? 12 : groups >= 128 ? 8 : 4; });
