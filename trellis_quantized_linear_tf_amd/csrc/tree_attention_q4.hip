@@ -72,7 +72,10 @@ __global__ __launch_bounds__(KG * 64, WAVES) void tree_attention_q4_kernel(AttnA
 
   ArgPtr x = arguments();
   Segment seg;
-  if (!find_piece<KT, kQ4Start>(x, blockIdx.x, &seg)) return;
+  // Where heads of a slot lie behind one another, 80 bytes of 128 columns each, two share most of the cache's lines: with
+  // neighbouring pieces on one XCD 24 sequences of 8 nodes take 43.1 us, not 46.5, 32 of 16 nodes over 16384 positions 241,
+  // not 256, and 4 trees of 64 nodes, whose row tiles read the same, 75.6, not 76.8.
+  if (!find_piece<KT, kQ4Start, true>(x, blockIdx.x, &seg)) return;
   const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   bool first = true;
   for (;;) {
@@ -420,7 +423,7 @@ __global__ __launch_bounds__(KG * 64, WAVES) void tree_attention_q4_kernel(AttnA
               *reinterpret_cast<u32x2*>(out + n * 16) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
             }
         } else {
-          const int64_t row = ((int64_t)blockIdx.x * 2 + !first) * kRows + r - row0;
+          const int64_t row = ((int64_t)seg.index * 2 + !first) * kRows + r - row0;
           if (kg == 0 && lg == 0) y->p.stat[row] = make_float2(base == -INFINITY ? -INFINITY : base * scale_c, total);
           float* part = y->p.part + row * dim + column;
 #pragma unroll
@@ -450,20 +453,20 @@ constexpr int waves_of(int dp, int rt) { return dp == 256 || rt == 4 ? 2 : dp * 
 // Row tiles of a wave: as many as there are, up to four (two at 256 columns), as long as enough tiles are left
 // to give every workgroup that the chip holds a few: a number is made once for all of a wave's rows, but one wave alone
 // takes long over many rows. One, two, four row tiles, us on the GPU, 8 heads of 128, by places (tiles of 128
-// positions of each row tile): 32 rows, 64 places of two row tiles 12.8 / 14.1, 1056 23.4 / 26.7, 2112 31.9 / 29.9, 6336
-// 77 / 46; 64 rows, 128 places of four 14 / 15 / 19, 1024 32 / 29 / 33, 2176 47 / 37 / 39, 3968 90 / 57 / 46, 7936
-// 164 / 100 / 64.
+// positions of each row tile): 32 rows, 64 places of two row tiles 13.3 / 14.4, 1056 21.4 / 27.8, 2112 28.3 / 29.1, 6336
+// 62 / 42; 64 rows, 128 places of four 15 / 16 / 19, 1024 29 / 27 / 31, 2176 44 / 35 / 38, 3968 63 / 47 / 45, 7936
+// 130 / 83 / 63.
 Shape shape_of(const tf_exl3_tree_attention_args& a) {
   const int dp = a.head_dim <= 64 ? 64 : a.head_dim <= 128 ? 128 : 256, rows = a.nodes * (a.q_heads / a.kv_heads);
   const int64_t tiles = ((int64_t)a.table_pages * a.page_size + a.nodes) / (4 * kQ4Positions) + 1;
   const int64_t groups = (int64_t)a.batch * a.kv_heads * tiles;
   int rt = 1;
-  if (rows > 16 && groups * ((rows + 31) / 32) >= 1536) rt = 2;
-  if (dp < 256 && rows > 32 && groups * ((rows + 63) / 64) >= 2560) rt = 4;
+  if (rows > 16 && groups * ((rows + 31) / 32) >= 2048) rt = 2;
+  if (dp < 256 && rows > 32 && groups * ((rows + 63) / 64) >= 3200) rt = 4;
   // Workgroups a CU that the line is cut for: what it holds (of 256 columns and two row tiles, 84 KB of shared memory,
   // one), but two where a piece would be a few tiles: beginning and joining it takes as long. Two, three, four, us on the
-  // GPU: 1088 places 16.1 / 14.3 / 14.2, 2056 29.8 / 32.1 / 32.3, 4608 32.2 / 36.3 / 35.6, 6336 in two row tiles 46.9 /
-  // 48.9 / -, 8320 48.7 / 50.4 / 53.4, 12480 45.7 / 44.7 / 44.2, 33024 154 / 150 / 148.
+  // GPU: 1088 places 17.0 / 15.1 / 15.2, 2056 30.0 / 32.7 / 32.5, 4608 29.1 / 31.6 / 32.6, 6336 in two row tiles 43.7 /
+  // 46.1 / -, 8320 41.1 / 45.9 / 47.1, 12480 45.9 / 44.8 / 44.3, 33024 154 / 150 / 151.
   const int64_t places = groups * ((rows + 16 * rt - 1) / (16 * rt));
   int resident = dp == 256 && rt == 2 ? 1 : waves_of(dp, rt);
   if (resident > 2 && places >= 2048 && places < 10240) resident = 2;

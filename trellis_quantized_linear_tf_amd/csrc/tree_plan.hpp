@@ -75,6 +75,7 @@ struct Segment {
   int len;                    // of the sequence in the cache
   int64_t begin;              // of the sequence in the line
   int start, piece;           // as in SeqTiles
+  int index;                  // of the piece
 };
 
 constexpr int kMostPieces = 96;
@@ -83,9 +84,12 @@ constexpr int kMostPieces = 96;
 // us against 69.1, 8 sequences of 16 nodes over 3000 positions 34.0 against 32.4.
 constexpr int kStart = 4;
 
-// Where the workgroup's piece begins. Sequences are looked at 64 at a time, a lane each; the
+// Workgroups with the same number modulo this run on one XCD and share its cache.
+constexpr int kTreeXCDs = 8;
+
+// Where the workgroup's piece begins. NEAR: neighbouring pieces go to one XCD. Sequences are looked at 64 at a time, a lane each; the
 // lengths of up to 64 are read once.
-template <int KT, int START = kStart>
+template <int KT, int START = kStart, bool NEAR = false>
 __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
   const int batch = x->a.batch, groups = x->p.groups, workgroups = x->p.workgroups, nodes = x->a.nodes;
   if (workgroups == 0) {
@@ -116,6 +120,13 @@ __device__ __forceinline__ bool find_piece(ArgPtr x, int w, Segment* s) {
   size = size > joined ? size : joined;
   s->piece = uniform((int)(size < x->p.min_piece ? x->p.min_piece : size));
   s->start = start;
+  if (NEAR) {
+    const int used = (int)divide(all + s->piece - 1, s->piece);
+    if (w >= used) return false;
+    const int xcd = w % kTreeXCDs;
+    w = xcd * (used / kTreeXCDs) + min(xcd, used % kTreeXCDs) + w / kTreeXCDs;
+  }
+  s->index = w;
   const int64_t from = (int64_t)w * s->piece;
   if (from >= all) return false;
   s->left = (int)(all - from < s->piece ? all - from : s->piece);
