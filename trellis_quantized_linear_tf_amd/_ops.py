@@ -81,6 +81,15 @@ def _followed(*tensors) -> bool:
         t is not None and forward.unpack_dual(t).tangent is not None for t in tensors)
 
 
+def _refuse_followed(*tensors) -> None:
+    """For tensors that a call with out= may not have in autograd's graph: what it writes there is in no graph, and a graph
+    that goes through what was there before would not know of it."""
+    if _followed(*tensors):
+        raise ValueError(
+            "out cannot be given here where autograd follows a tensor: call it without out, under torch.no_grad() or on "
+            "detached tensors")
+
+
 @functools.cache
 def _nodes():
     """The calls' nodes in autograd's graph. None has a forward mode, which autograd itself refuses then."""
@@ -182,7 +191,7 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
     scale defaults to dim ** -0.5. A node that sees nothing gets zeros.
 
     It has no gradient: where autograd follows an input, the result (not `out` itself) is part of
-    its graph, and a backward pass that reaches it raises."""
+    its graph, and a backward pass that reaches it raises. An `out` that autograd follows is refused."""
     torch = _torch()
     dev = -1
     try:
@@ -215,6 +224,8 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
         _check_tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, out)
     if out is None:
         out = q.new_empty(shape)
+    else:
+        _refuse_followed(out)
     lib = load()
     a = _lib.TreeAttentionArgs(_dt_code(t), batch, nodes, hq, hkv, dim, pages[0], pages[1], columns)
     need = lib.tf_exl3_tree_attention_workspace(a)

@@ -6,8 +6,9 @@ Marshalling only, as in _ops: every argument is checked here, outputs and the wo
 from torch's allocator on the current stream, and the library's kernels do the rest on that
 stream. The formulas, and what happens to out-of-range values on the device, stand in
 include/tf_exl3.h. None of these calls has a gradient: where autograd follows an input, the
-results are part of its graph, and a backward pass that reaches them raises. The cache takes
-values: to autograd its rows are constants.
+results are part of its graph, and a backward pass that reaches them raises; with out=, a call is
+refused where autograd follows an input or the buffer. The cache takes values: to autograd its
+rows are constants.
 """
 
 from __future__ import annotations
@@ -26,6 +27,7 @@ from ._ops import (
     _one_gpu,
     _pack,
     _ptr,
+    _refuse_followed,
     _whole,
     _workspace,
 )
@@ -92,7 +94,8 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
     fused projection's rows will do. frequencies fp32 [rotary_dim / 2], radians a position; the
     pairs are (f, f + rotary_dim / 2), or (2f, 2f + 1) where interleaved; None turns nothing
     (positions are not looked at). q_weight, k_weight [dim], None for ones. eps None: no norm,
-    and no weights. out: the pair of results, which may be (q, k) themselves."""
+    and no weights. out: the pair of results, which may be (q, k) themselves; refused where autograd
+    follows any of the tensors."""
     torch = _torch()
     q_out, k_out = (None, None) if out is None else _pair(out)
     if eps is None and not (q_weight is None and k_weight is None):
@@ -121,6 +124,8 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
         _check_norm_rotate(q, k, positions, frequencies, q_weight, k_weight, (q_out, k_out))
         shape, rows = q.shape, k.shape
         w = k_weight if q_weight is None else q_weight
+    if out is not None:
+        _refuse_followed(q, k, q_weight, k_weight, q_out, k_out)
     if q_out is None:
         q_out = q.new_empty(shape)
     if k_out is None:
@@ -171,8 +176,8 @@ def prompt_attention(q, k, v, offsets, scale=None, out=None):
     q [tokens][q_heads][dim], k and v [tokens][kv_heads][dim] of fp16 or bf16 (views of a fused
     projection's rows will do); offsets int32 [batch + 1]: sequence b has the tokens offsets[b] ..
     offsets[b + 1] - 1, and each sees those of its sequence up to itself. Rows outside of all
-    sequences are left as they are in `out` (without one: not set). scale defaults to
-    dim ** -0.5. How long the sequences are is not looked at on the host, so a captured call
+    sequences are left as they are in `out` (without one: not set; refused where autograd follows a
+    tensor). scale defaults to dim ** -0.5. How long the sequences are is not looked at on the host, so a captured call
     can be replayed with other offsets."""
     torch = _torch()
     dev = -1
@@ -196,6 +201,8 @@ def prompt_attention(q, k, v, offsets, scale=None, out=None):
         rows = k.shape
     if out is None:
         out = q.new_empty(shape)
+    else:
+        _refuse_followed(q, k, v, out)
     a = _lib.PromptAttentionArgs()
     _pack(
         _PROMPT, a, _dt_code(q.dtype), tokens, offsets.shape[0] - 1, heads, rows[1], dim,
@@ -342,7 +349,8 @@ def _check_tree_attention_q4(q, k, v, mask, k_cache, v_cache, table, lengths, ou
 def tree_attention_q4(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, out=None):
     """tree_attention over a cache in 4 bits (tf_exl3_tree_attention_q4): k_cache, v_cache uint8
     [pages][page_size][kv_heads][q4_row_bytes(dim)] as in cache_append_q4, everything else as
-    in tree_attention. A cached row is what cache_read_q4 gives in q's type."""
+    in tree_attention, but that `out` is refused where autograd follows a tensor. A cached row is what
+    cache_read_q4 gives in q's type."""
     torch = _torch()
     fit = False
     try:
@@ -366,6 +374,8 @@ def tree_attention_q4(q, k, v, mask, k_cache, v_cache, table, lengths, scale=Non
         hkv = k.shape[2]
     if out is None:
         out = q.new_empty(shape)
+    else:
+        _refuse_followed(q, k, v, out)
     lib = load()
     pages, columns = k_cache.shape, table.shape[1]
     a = _lib.TreeAttentionArgs(_dt_code(q.dtype), batch, nodes, hq, hkv, dim, pages[0], pages[1], columns)
