@@ -9,7 +9,7 @@ import trellis_quantized_linear_tf_amd as tq
 from tests.test_argument_checks_host import Near
 from tests.test_argument_checks_host import attention as attention16
 from tests.test_other_gpu_host import machine  # noqa: F401
-from tests.test_rows_host import attention, packed, prompt, rotate
+from tests.test_rows_host import append, attention, packed, prompt, rotate
 from trellis_quantized_linear_tf_amd import _ops, _rows
 
 INTO = {"norm_rotate": (tq.norm_rotate, rotate), "norm_rotate packed": (tq.norm_rotate, packed),
@@ -87,3 +87,45 @@ def test_one_buffer_of_two(machine):  # noqa: F811
         tq.norm_rotate(**dict(a, out=(None, into)))
     a["q"].requires_grad_(False)
     assert tq.norm_rotate(**dict(a, out=(None, into)))[1] is into
+
+
+# ---------------------------------------------------------------- versions
+
+
+def append_args():
+    a = attention16()
+    return {n: a[n] for n in ("k", "v", "k_cache", "v_cache", "table", "lengths")}
+
+
+WRITERS = {**INTO, "cache_append": (tq.cache_append, append_args), "cache_append_q4": (tq.cache_append_q4, append)}
+
+
+@pytest.mark.parametrize("name", WRITERS)
+def test_what_is_written_is_known_to_have_changed(machine, name):  # noqa: F811
+    call, make = WRITERS[name]
+    a = near(make) if name in INTO else {n: t.as_subclass(Near) for n, t in make().items()}
+    outs = a.get("out", (a.get("k_cache"), a.get("v_cache")))
+    outs = outs if isinstance(outs, tuple) else (outs,)
+    others = [t for n, t in a.items() if n != "out" and all(t is not o for o in outs)]
+    before, still = [o._version for o in outs], [t._version for t in others]
+    call(**a)
+    assert all(o._version > n for o, n in zip(outs, before)) and [t._version for t in others] == still
+
+
+def test_a_backward_pass_that_needs_overwritten_rows_fails(machine):  # noqa: F811
+    """s = sum q q keeps q, and q is turned in place before s's backward pass."""
+    a = near(rotate)
+    w = torch.ones_like(a["q"]).requires_grad_()
+    s = (w * a["q"]).sum()
+    tq.norm_rotate(**dict(a, out=(a["q"], a["k"])))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        s.backward()
+
+
+def test_buffers_of_inference_mode(machine):  # noqa: F811
+    """They have no version."""
+    with torch.inference_mode():
+        for name in WRITERS:
+            call, make = WRITERS[name]
+            call(**(near(make) if name in INTO else {n: t.as_subclass(Near) for n, t in make().items()}))
+    assert len(machine.calls) == len(WRITERS)

@@ -90,6 +90,11 @@ def _refuse_followed(*tensors) -> None:
             "detached tensors")
 
 
+def _changed(*tensors) -> None:
+    """Raises the versions of tensors that a call has written into: a backward pass that needs what was there fails."""
+    _torch().autograd.graph.increment_version(tensors)
+
+
 @functools.cache
 def _nodes():
     """The calls' nodes in autograd's graph. None has a forward mode, which autograd itself refuses then."""
@@ -222,10 +227,11 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
         pass
     if dev < 0:
         _check_tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, out)
-    if out is None:
-        out = q.new_empty(shape)
-    else:
+    given = out is not None
+    if given:
         _refuse_followed(out)
+    else:
+        out = q.new_empty(shape)
     lib = load()
     a = _lib.TreeAttentionArgs(_dt_code(t), batch, nodes, hq, hkv, dim, pages[0], pages[1], columns)
     need = lib.tf_exl3_tree_attention_workspace(a)
@@ -236,6 +242,8 @@ def tree_attention(q, k, v, mask, k_cache, v_cache, table, lengths, scale=None, 
         k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), out.data_ptr(), ws.data_ptr(), need,
         *sq[:3], *sk[:3], *sv[:3], *skc[:3], *svc[:3], *out.stride()[:3], table.stride(0))
     _run(q, lib.tf_exl3_tree_attention, a)
+    if given:
+        _changed(out)
     if _followed(q, k, v, k_cache, v_cache):
         return _nodes()[0].apply("tree_attention", out, q, k, v, k_cache, v_cache)
     return out
@@ -298,6 +306,7 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=None
         k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), _ptr(nodes) or 0, _ptr(counts) or 0,
         *sk[:3], *sv[:3], *skc[:3], *svc[:3], table.stride(0))
     _run(k, load().tf_exl3_cache_append, a)
+    _changed(k_cache, v_cache)
 
 
 def _check_drafts(logits, tokens, u, temperature):

@@ -19,6 +19,7 @@ from . import _lib
 from ._lib import _dt_code, _run, _torch, load
 from ._ops import (
     _ATTENTION,
+    _changed,
     _floats,
     _followed,
     _halves,
@@ -146,6 +147,8 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
         0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), angles[1], angles[2],
         q_out.data_ptr(), k_out.data_ptr(), *steps)
     _run(q, load().tf_exl3_norm_rotate, a)
+    if out is not None:
+        _changed(q_out, k_out)
     if _followed(q, k, q_weight, k_weight):
         return tuple(_without_gradient("norm_rotate", o, x, y) for o, x, y in ((q_out, q, q_weight), (k_out, k, k_weight)))
     return q_out, k_out
@@ -199,16 +202,19 @@ def prompt_attention(q, k, v, offsets, scale=None, out=None):
         _check_prompt_attention(q, k, v, offsets, out)
         tokens, heads, dim = shape = q.shape
         rows = k.shape
-    if out is None:
-        out = q.new_empty(shape)
-    else:
+    given = out is not None
+    if given:
         _refuse_followed(q, k, v, out)
+    else:
+        out = q.new_empty(shape)
     a = _lib.PromptAttentionArgs()
     _pack(
         _PROMPT, a, _dt_code(q.dtype), tokens, offsets.shape[0] - 1, heads, rows[1], dim,
         dim ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), offsets.data_ptr(), out.data_ptr(),
         *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *out.stride()[:2])
     _run(q, load().tf_exl3_prompt_attention, a)
+    if given:
+        _changed(out)
     if _followed(q, k, v):
         return _without_gradient("prompt_attention", out, q, k, v)
     return out
@@ -287,6 +293,7 @@ def cache_append_q4(k, v, k_cache, v_cache, table, lengths, nodes=None, counts=N
         v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lengths.data_ptr(), _ptr(nodes) or 0,
         _ptr(counts) or 0, *k.stride()[:3], *v.stride()[:3], *k_cache.stride()[:3], *v_cache.stride()[:3], table.stride(0))
     _run(k, load().tf_exl3_cache_append_q4, a)
+    _changed(k_cache, v_cache)
 
 
 def cache_read_q4(k_cache, v_cache, table, lengths, tokens, first=None, dtype=None):
@@ -372,10 +379,11 @@ def tree_attention_q4(q, k, v, mask, k_cache, v_cache, table, lengths, scale=Non
         _check_tree_attention_q4(q, k, v, mask, k_cache, v_cache, table, lengths, out)
         batch, nodes, hq, dim = shape = q.shape
         hkv = k.shape[2]
-    if out is None:
-        out = q.new_empty(shape)
-    else:
+    given = out is not None
+    if given:
         _refuse_followed(q, k, v, out)
+    else:
+        out = q.new_empty(shape)
     lib = load()
     pages, columns = k_cache.shape, table.shape[1]
     a = _lib.TreeAttentionArgs(_dt_code(q.dtype), batch, nodes, hq, hkv, dim, pages[0], pages[1], columns)
@@ -388,6 +396,8 @@ def tree_attention_q4(q, k, v, mask, k_cache, v_cache, table, lengths, scale=Non
         *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *k_cache.stride()[:3], *v_cache.stride()[:3], *out.stride()[:3],
         table.stride(0))
     _run(q, lib.tf_exl3_tree_attention_q4, a)
+    if given:
+        _changed(out)
     if _followed(q, k, v):
         return _without_gradient("tree_attention_q4", out, q, k, v)
     return out
