@@ -475,7 +475,8 @@ size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k);
  *                [head_dim] or NULL: all ones); any of the three
  *   q, k         [batch][tokens][heads][head_dim], strides [batch, token, head], below 2^32
  *   q_out, k_out likewise; each may be its input itself (the same pointer and strides), else
- *                they overlap no input; rows of q and k may alternate in one buffer
+ *                they overlap no input; rows of q and k may alternate in one buffer, token by token or
+ *                sequence by sequence (heads in front of tokens), at the same steps
  *   positions    int32 [batch][tokens], rows positions_stride apart
  *   frequencies  fp32 [rotary_dim / 2] (NULL if rotary_dim is 0)
  *   head_dim     a multiple of 16 up to 512; rotary_dim a multiple of 16 up to head_dim

@@ -168,3 +168,15 @@ def test_gradient_is_refused_when_asked_for(gpu):
     assert out[0].requires_grad
     with pytest.raises(RuntimeError, match="norm_rotate has no gradient"):
         out[0].sum().backward()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_heads_first_rows_in_place(gpu, dt):
+    """[batch][heads][tokens][dim] of a fused projection, a sequence's queries, then its keys, then its values."""
+    x, q, k, pos, freq, w = inputs(6, dt, (3, 17), 4, 2, 128, 64)
+    xg = x.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    views = xg.split([4, 2, 2], dim=-2)
+    tq.norm_rotate(*views[:2], pos.cuda(), freq.cuda(), *(a.cuda() for a in w), out=views[:2])
+    check(xg[..., :4, :], q, w[0], pos, freq, 1e-6, False, dt)
+    check(xg[..., 4:6, :], k, w[1], pos, freq, 1e-6, False, dt)
+    assert torch.equal(xg[..., 6:, :].cpu(), x[..., 6:, :])

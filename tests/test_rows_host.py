@@ -286,3 +286,68 @@ def test_argument_structures_have_the_headers_layout(tmp_path):
     subprocess.run([cc, "-std=c11", f"-I{_lib.PKG.parent / 'include'}", str(src), "-o", str(tmp_path / "layout")], check=True)
     got = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.split()
     assert [int(g) for g in got] == want
+
+
+# Calls that are accepted go on to the launch: only where there is no GPU for it.
+no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="would launch with addresses of nothing")
+
+# Heads in front of tokens, [batch][heads][tokens][dim]: a sequence's queries, then its keys, in one buffer.
+HEADS, TOKENS = (4, 2), 3
+FIRST = dict(q_stride=(8 * TOKENS * 64, 64, TOKENS * 64), k_stride=(8 * TOKENS * 64, 64, TOKENS * 64))
+FIRST |= dict(q_out_stride=FIRST["q_stride"], k_out_stride=FIRST["k_stride"], q=FAKE, q_out=FAKE)
+BLOCK = HEADS[0] * TOKENS * 128  # bytes of a sequence's queries
+
+
+@no_gpu
+@pytest.mark.parametrize("behind,fine", [(0, True), (-2, False), (2 * TOKENS * 128, True), (2 * TOKENS * 128 + 2, False), (128, True)])
+def test_heads_first_rows_that_alternate_in_one_buffer(lib, behind, fine):  # noqa: F811
+    """Where they do not meet the call goes on to the launch, which has no GPU here."""
+    k = FAKE + BLOCK + behind
+    status = lib.tf_exl3_norm_rotate(rotate_args(**FIRST, k=k, k_out=k), None)
+    assert status == (-9 if fine else -7)
+    swapped = FIRST | dict(q=k, q_out=k, q_stride=FIRST["k_stride"], q_heads=HEADS[1], kv_heads=HEADS[0])
+    assert lib.tf_exl3_norm_rotate(rotate_args(**swapped, k=FAKE, k_out=FAKE), None) == status
+
+
+@no_gpu
+def test_sequences_that_alternate_by_token(lib):  # noqa: F811
+    """[tokens][heads][batch][dim]."""
+    strides = (64, 8 * 2 * 64, 2 * 64)
+    kw = dict(q_stride=strides, k_stride=strides, q_out_stride=strides, k_out_stride=strides, q=FAKE, q_out=FAKE)
+    for k, status in ((4 * 256, -9), (4 * 256 - 2, -7), (6 * 256, -9), (6 * 256 + 2, -7)):
+        assert lib.tf_exl3_norm_rotate(rotate_args(**kw, k=FAKE + k, k_out=FAKE + k), None) == status
+
+
+@no_gpu
+def test_alternating_rows_by_brute_force(lib):  # noqa: F811
+    """Small buffers in every order of batch, tokens and heads with the keys at every place: refused wherever a byte is in a
+    query row and in a key row, and accepted where each set fits behind the other within a step."""
+    import itertools
+
+    r = random.Random(5)
+    accepted = 0
+    for _ in range(400):
+        batch, tokens, hq, hkv, dim = r.randint(1, 3), r.randint(1, 3), r.randint(1, 3), r.randint(1, 3), 16
+        order = r.choice(list(itertools.permutations(range(3))))
+        sizes = [batch, tokens, hq + hkv]
+        strides, step = [0, 0, 0], dim
+        for axis in reversed(order):
+            strides[axis] = step
+            step *= sizes[axis]
+        at = r.choice([hq * strides[2], r.randrange(0, step)])
+
+        def bytes_of(first, heads):
+            return {first + b * strides[0] + t * strides[1] + h * strides[2] + d
+                    for b in range(batch) for t in range(tokens) for h in range(heads) for d in range(dim)}
+
+        meet = bool(bytes_of(0, hq) & bytes_of(at, hkv))
+        kw = dict(q_stride=strides, k_stride=strides, q_out_stride=strides, k_out_stride=strides)
+        kw = {n: tuple(s) for n, s in kw.items()}
+        a = rotate_args(batch=batch, tokens=tokens, q_heads=hq, kv_heads=hkv, head_dim=dim, rotary_dim=16, q=FAKE, q_out=FAKE,
+                        k=FAKE + 2 * at, k_out=FAKE + 2 * at, **kw)
+        status = lib.tf_exl3_norm_rotate(a, None)
+        assert status == -7 if meet else status in (-7, -9)
+        if at == hq * strides[2]:
+            assert not meet and status == -9, (order, sizes, hq)
+        accepted += status == -9
+    assert accepted > 100

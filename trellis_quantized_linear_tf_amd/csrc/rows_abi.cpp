@@ -13,18 +13,23 @@ namespace {
 constexpr int kMostHeads = 65535;
 constexpr int kMostTokens = 1 << 30;
 
-// Whether heads of two sets of rows alternate in one buffer: the same steps from token to token and from
-// sequence to sequence, and a token's heads of the one, then of the other, within a step.
+// Whether two sets of rows alternate in one buffer: of each sequence, of each token, or of each token of each sequence
+// the one set's part, then the other's, within a step from one to the next that both have.
 bool alternate(const void* a, int heads_a, const int64_t* sa, const void* b, int heads_b, const int64_t* sb, int64_t batch,
                int64_t tokens, int64_t dim, int64_t e) {
   if ((uintptr_t)a > (uintptr_t)b) return alternate(b, heads_b, sb, a, heads_a, sa, batch, tokens, dim, e);
-  if (sa[0] != sb[0] || sa[1] != sb[1]) return false;
   const int64_t between = (int64_t)((uintptr_t)b - (uintptr_t)a);
-  const int64_t one = ((heads_a - 1) * sa[2] + dim) * e, other = ((heads_b - 1) * sb[2] + dim) * e;
-  if (between < one) return false;
-  if (tokens > 1 && between + other > sa[1] * e) return false;
-  if (batch > 1 && between + other > sa[0] * e) return false;
-  return batch <= 1 || tokens <= 1 || sa[0] >= tokens * sa[1] || sa[1] >= batch * sa[0];
+  // n0 x n1 rows of all heads, a step apart from the next such part.
+  auto within = [&](int64_t step, int64_t n0, int64_t n1) {
+    const int64_t one = (n0 - 1) * sa[0] + (n1 - 1) * sa[1] + (heads_a - 1) * sa[2] + dim;
+    const int64_t other = (n0 - 1) * sb[0] + (n1 - 1) * sb[1] + (heads_b - 1) * sb[2] + dim;
+    return between >= one * e && between + other * e <= step * e;
+  };
+  const bool sequences = batch > 1 && sa[0] == sb[0], each_token = tokens > 1 && sa[1] == sb[1];
+  if (sequences && within(sa[0], 1, tokens)) return true;
+  if (each_token && within(sa[1], batch, 1)) return true;
+  if (!sequences || !each_token) return false;
+  return (sa[0] >= tokens * sa[1] && within(sa[1], 1, 1)) || (sa[1] >= batch * sa[0] && within(sa[0], 1, 1));
 }
 
 bool q4_dim_ok(int head_dim) { return head_dim >= 32 && head_dim % 32 == 0 && head_dim <= (1 << 24); }
