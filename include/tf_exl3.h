@@ -469,7 +469,7 @@ size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k);
  * rotary_dim on are y, cast. Sums and products are in fp32, rounded once to the type at the
  * end; t is formed and reduced to a part of a turn in 64 bits, so far positions keep
  * fp32's accuracy.
- * A row's squares are summed in fp32: elements past about 10^18 make a row of zeros.
+ * However small or large a row's elements are, its squares' mean keeps fp32's accuracy.
  *
  *   dtype        of q, k and the outputs; weight_dtype of q_weight and k_weight (each
  *                [head_dim] or NULL: all ones); any of the three

@@ -180,3 +180,22 @@ def test_heads_first_rows_in_place(gpu, dt):
     check(xg[..., :4, :], q, w[0], pos, freq, 1e-6, False, dt)
     check(xg[..., 4:6, :], k, w[1], pos, freq, 1e-6, False, dt)
     assert torch.equal(xg[..., 6:, :].cpu(), x[..., 6:, :])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("spread", [1e-36, 1e-30, 1e-24, 1e-20, 1e-18, 1e17, 1e19, 1e24, 1e30, 1e36])
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-6])
+def test_rows_whose_squares_leave_fp32(gpu, dt, spread, eps):
+    run(dt, (2, 9), 4, 2, 128, 64, spread=spread, eps=eps)
+
+
+@pytest.mark.parametrize("dim", [16, 64, 256, 512])
+def test_rows_of_many_sizes_beside_each_other(gpu, dim):
+    """Rows of every size share a wave with rows of others."""
+    x, q, k, pos, freq, w = inputs(8, "f32", (40,), 4, 2, dim, 16)
+    sizes = 10.0 ** torch.linspace(-36, 36, 40)[torch.randperm(40, generator=torch.Generator().manual_seed(1))]
+    x = x * sizes[:, None, None]
+    q, k, _ = x.split([4, 2, 2], dim=-2)
+    out = tq.norm_rotate(q.cuda(), k.cuda(), pos.cuda(), freq.cuda(), *(a.cuda() for a in w), eps=0.0)
+    check(out[0], q, w[0], pos, freq, 0.0, False, "f32")
+    check(out[1], k, w[1], pos, freq, 0.0, False, "f32")

@@ -50,15 +50,24 @@ __device__ __forceinline__ void load_weights(const void* w, int dtype, int at, f
     load8<TF_DT_BF16>(static_cast<const uint16_t*>(w) + at, x);
 }
 
-// Sum over aligned groups of LANES lanes, the same in each of them.
-template <int LANES>
-__device__ __forceinline__ float lanes_sum(float v) {
-  v += dpp<0xB1, 0xF>(v, 0.f);                           // lanes 1 apart
-  v += dpp<0x4E, 0xF>(v, 0.f);                           // 2 apart
-  if constexpr (LANES >= 8) v += dpp<0x141, 0xF>(v, 0.f);   // mirrored in 8: the other four
-  if constexpr (LANES >= 16) v += dpp<0x140, 0xF>(v, 0.f);  // mirrored in 16: the other eight
-  if constexpr (LANES >= 32) v += __shfl_xor(v, 16);
+// f over aligned groups of LANES lanes, the same in each of them.
+template <int LANES, typename F>
+__device__ __forceinline__ float lanes_join(float v, F f) {
+  v = f(v, dpp<0xB1, 0xF>(v, 0.f));                           // lanes 1 apart
+  v = f(v, dpp<0x4E, 0xF>(v, 0.f));                           // 2 apart
+  if constexpr (LANES >= 8) v = f(v, dpp<0x141, 0xF>(v, 0.f));   // mirrored in 8: the other four
+  if constexpr (LANES >= 16) v = f(v, dpp<0x140, 0xF>(v, 0.f));  // mirrored in 16: the other eight
+  if constexpr (LANES >= 32) v = f(v, __shfl_xor(v, 16));
   return v;
+}
+
+// Mean of the row's squares.
+template <int LANES>
+__device__ __forceinline__ float mean_square(const float (&x)[8], const float (&y)[8], int dim) {
+  float squares = 0.f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) squares = __builtin_fmaf(x[n], x[n], __builtin_fmaf(y[n], y[n], squares));
+  return lanes_join<LANES>(squares, [](float u, float v) { return u + v; }) / (float)dim;
 }
 
 template <int DT, int LANES>
@@ -149,11 +158,21 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
           load_weights(w, a.weight_dtype, at1, w1);
         }
       }
-      float squares = 0.f;
+      float square = mean_square<LANES>(x, y, a.head_dim) + a.eps;
+      // Squares near the ends of fp32: the row, and the square root of eps, in units of a power of two in which the largest
+      // of them is about 1. All of a row's lanes come here together. (Squares of fp16 are far from them.)
+      if (DT != TF_DT_F16 && !(square > 0x1p-80f && square < 0x1p120f)) {
+        float most = sqrtf(a.eps);
 #pragma unroll
-      for (int n = 0; n < 8; ++n) squares = __builtin_fmaf(x[n], x[n], __builtin_fmaf(y[n], y[n], squares));
-      squares = lanes_sum<LANES>(squares);
-      const float scale = 1.f / sqrtf(squares / (float)a.head_dim + a.eps);
+        for (int n = 0; n < 8; ++n) most = fmaxf(most, fmaxf(fabsf(x[n]), fabsf(y[n])));
+        most = lanes_join<LANES>(most, [](float u, float v) { return fmaxf(u, v); });
+        // 0 for 0 and infinity, whose rows stay what they are
+        const float unit = ldexpf(1.f, min(max(-__builtin_amdgcn_frexp_expf(most), -126), 126));
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x[n] *= unit, y[n] *= unit;
+        square = mean_square<LANES>(x, y, a.head_dim) + a.eps * unit * unit;
+      }
+      const float scale = 1.f / sqrtf(square);
 #pragma unroll
       for (int n = 0; n < 8; ++n) x[n] = x[n] * scale * w0[n], y[n] = y[n] * scale * w1[n];
     }
