@@ -199,3 +199,32 @@ def test_rows_of_many_sizes_beside_each_other(gpu, dim):
     out = tq.norm_rotate(q.cuda(), k.cuda(), pos.cuda(), freq.cuda(), *(a.cuda() for a in w), eps=0.0)
     check(out[0], q, w[0], pos, freq, 0.0, False, "f32")
     check(out[1], k, w[1], pos, freq, 0.0, False, "f32")
+
+
+@pytest.mark.parametrize("tokens", [(1, 1), (4, 300)])
+def test_in_a_graph(gpu, tokens):
+    """A captured call in place and one with results of its own, replayed over other rows and positions, with
+    eager work in between."""
+    x, q, k, pos, freq, w = inputs(11, "bf16", tokens, 4, 2, 128, 64)
+    xg, posg, freqg, wg = torch.empty_like(x, device="cuda"), pos.cuda(), freq.cuda(), [a.cuda() for a in w]
+    views = xg.split([4, 2, 2], dim=-2)[:2]
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        xg.copy_(x)
+        tq.norm_rotate(*views, posg, freqg, *wg)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        apart = tq.norm_rotate(*views, posg, freqg, *wg)
+        tq.norm_rotate(*views, posg, freqg, *wg, out=views)
+    for seed in (11, 12, 13, 11):
+        x, q, k, pos, _, _ = inputs(seed, "bf16", tokens, 4, 2, 128, 64)
+        xg.copy_(x)
+        posg.copy_(pos)
+        eager = tq.norm_rotate(*views, posg, freqg, *wg)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, there, want in zip(apart, views, eager):
+            assert torch.equal(got, want) and torch.equal(there, want)
+        check(eager[0], q, w[0], pos, freq, 1e-6, False, "bf16")
+        assert torch.equal(xg[..., 6:, :].cpu(), x[..., 6:, :])
