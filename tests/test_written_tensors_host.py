@@ -129,3 +129,20 @@ def test_buffers_of_inference_mode(machine):  # noqa: F811
             call, make = WRITERS[name]
             call(**(near(make) if name in INTO else {n: t.as_subclass(Near) for n, t in make().items()}))
     assert len(machine.calls) == len(WRITERS)
+
+
+@pytest.mark.parametrize("name", ["norm_rotate", "norm_rotate packed"])
+@pytest.mark.parametrize("which", ["q", "k", "frequencies", "q_weight", "k_weight"])
+def test_rotation_has_no_backward_pass(machine, name, which):  # noqa: F811
+    call, make = INTO[name]
+    a = near(make)
+    into = a.pop("out")
+    a[which].requires_grad_()
+    out = call(**a)
+    assert [o.requires_grad for o in out] == [which not in ("k", "k_weight"), which not in ("q", "q_weight")]
+    with pytest.raises(RuntimeError, match="norm_rotate has no gradient"):
+        sum(o.float().sum() for o in out).backward()
+    with pytest.raises(ValueError, match="autograd follows"):
+        call(**a, out=into)
+    with torch.no_grad():
+        assert not any(o.requires_grad for o in call(**a))

@@ -126,7 +126,7 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
         shape, rows = q.shape, k.shape
         w = k_weight if q_weight is None else q_weight
     if out is not None:
-        _refuse_followed(q, k, q_weight, k_weight, q_out, k_out)
+        _refuse_followed(q, k, frequencies, q_weight, k_weight, q_out, k_out)
     if q_out is None:
         q_out = q.new_empty(shape)
     if k_out is None:
@@ -149,8 +149,9 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
     _run(q, load().tf_exl3_norm_rotate, a)
     if out is not None:
         _changed(q_out, k_out)
-    if _followed(q, k, q_weight, k_weight):
-        return tuple(_without_gradient("norm_rotate", o, x, y) for o, x, y in ((q_out, q, q_weight), (k_out, k, k_weight)))
+    if _followed(q, k, frequencies, q_weight, k_weight):
+        return tuple(_without_gradient("norm_rotate", o, x, frequencies, y)
+                     for o, x, y in ((q_out, q, q_weight), (k_out, k, k_weight)))
     return q_out, k_out
 
 
