@@ -479,7 +479,8 @@ size_t tf_exl3_distill_workspace(int dtype, int rows, int vocab, int top_k);
  *                sequence by sequence (heads in front of tokens), at the same steps
  *   positions    int32 [batch][tokens], rows positions_stride apart
  *   frequencies  fp32 [rotary_dim / 2] (NULL if rotary_dim is 0)
- *   head_dim     a multiple of 16 up to 512; rotary_dim a multiple of 16 up to head_dim
+ *   head_dim     a multiple of 16 up to 512; rotary_dim a multiple of 8 from 16 up to
+ *                head_dim, or 0
  *   batch * tokens below 2^24
  */
 typedef struct tf_exl3_norm_rotate_args {

@@ -228,3 +228,35 @@ def test_in_a_graph(gpu, tokens):
             assert torch.equal(got, want) and torch.equal(there, want)
         check(eager[0], q, w[0], pos, freq, 1e-6, False, "bf16")
         assert torch.equal(xg[..., 6:, :].cpu(), x[..., 6:, :])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,rotary", [(32, 24), (48, 24), (48, 40), (64, 24), (64, 56), (80, 72), (96, 24), (96, 88), (128, 24), (128, 120),
+                                        (160, 40), (256, 24), (256, 248), (320, 72), (512, 24), (512, 504)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_sizes_between_pieces(gpu, dt, dim, rotary, interleaved):
+    say(f"{dt} {dim} {rotary} {interleaved}")
+    run(dt, (2, 5), 3, 2, dim, rotary, interleaved=interleaved)
+    run(dt, (700,), 5, 1, dim, rotary, interleaved=interleaved, weights="f32" if dt == "f16" else None)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rotary_sizes_between_pieces_in_place(gpu, dt, interleaved):
+    x, q, k, pos, freq, w = inputs(5, dt, (3, 417), 4, 2, 96, 24)
+    xg = x.cuda()
+    views = xg.split([4, 2, 2], dim=-2)
+    tq.norm_rotate(*views[:2], pos.cuda(), freq.cuda(), *(a.cuda() for a in w), interleaved=interleaved, out=views[:2])
+    check(xg[..., :4, :], q, w[0], pos, freq, 1e-6, interleaved, dt)
+    check(xg[..., 4:6, :], k, w[1], pos, freq, 1e-6, interleaved, dt)
+    assert torch.equal(xg[..., 6:, :].cpu(), x[..., 6:, :])
+
+
+def test_infinities_beside_the_turned_part(gpu):
+    """What lies behind rotary_dim is not multiplied by any sine."""
+    for interleaved in (False, True):
+        x = torch.ones((3, 2, 96))
+        x[..., 24:32] = float("inf")
+        out = tq.norm_rotate(x.cuda(), x.cuda(), torch.arange(3, dtype=torch.int32).cuda(), torch.ones(12, device="cuda"), eps=None,
+                             interleaved=interleaved)[0].cpu()
+        assert torch.equal(out[..., 24:], x[..., 24:]) and out[..., :24].isfinite().all()

@@ -351,3 +351,10 @@ def test_alternating_rows_by_brute_force(lib):  # noqa: F811
             assert not meet and status == -9, (order, sizes, hq)
         accepted += status == -9
     assert accepted > 100
+
+
+@pytest.mark.parametrize("rotary", range(0, 66))
+def test_rotary_sizes(lib, rotary):  # noqa: F811
+    """Multiples of 8 from 16 on, or none."""
+    fine = rotary == 0 or 16 <= rotary <= 64 and rotary % 8 == 0
+    assert lib.tf_exl3_norm_rotate(rotate_args(rotary_dim=rotary, batch=0), None) == (0 if fine else -10)

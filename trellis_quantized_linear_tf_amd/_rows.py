@@ -92,9 +92,9 @@ def norm_rotate(q, k, positions, frequencies, q_weight=None, k_weight=None, eps=
 
     q [batch][tokens][q_heads][dim] and k [batch][tokens][kv_heads][dim] of fp32, fp16 or bf16 with
     positions int32 [batch][tokens], or all three without the batch: packed tokens. Views of a
-    fused projection's rows will do. frequencies fp32 [rotary_dim / 2], radians a position; the
-    pairs are (f, f + rotary_dim / 2), or (2f, 2f + 1) where interleaved; None turns nothing
-    (positions are not looked at). q_weight, k_weight [dim], None for ones. eps None: no norm,
+    fused projection's rows will do. frequencies fp32 [rotary_dim / 2], radians a position
+    (rotary_dim a multiple of 8 from 16 up to dim); the pairs are (f, f + rotary_dim / 2), or (2f, 2f + 1)
+    where interleaved; None turns nothing (positions are not looked at). q_weight, k_weight [dim], None for ones. eps None: no norm,
     and no weights. out: the pair of results, which may be (q, k) themselves; refused where autograd
     follows any of the tensors."""
     torch = _torch()

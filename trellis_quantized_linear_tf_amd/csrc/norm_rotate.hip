@@ -24,6 +24,8 @@ struct RotatePlan {
   FastDiv by_q_heads, by_kv_heads, by_tokens, by_angles;
 };
 
+typedef uint32_t u32x2_elem __attribute__((ext_vector_type(2), aligned(2)));
+
 // Two pieces of eight elements of a row, as they lie there.
 template <int DT>
 struct RawRow {
@@ -38,6 +40,29 @@ __device__ __forceinline__ void numbers(const u32x4 (&raw)[RawRow<DT>::kPieces],
     for (int i = 0; i < 8; ++i) x[i] = bits_to_f32(raw[i / 4][i % 4]);
   } else {
     Elem<DT>::unpack(raw[0], x);
+  }
+}
+
+// The same of a row whose last pair of turned pieces is half of each: elements 4 to 7 of a piece stand elsewhere.
+template <int DT>
+__device__ __forceinline__ void load_halves(const typename Elem<DT>::type* first, const typename Elem<DT>::type* last,
+                                            u32x4 (&raw)[RawRow<DT>::kPieces]) {
+  if constexpr (DT == TF_DT_F32) {
+    raw[0] = load_piece(first), raw[1] = load_piece(last);
+  } else {
+    const u32x2_elem a = *reinterpret_cast<const u32x2_elem*>(first), b = *reinterpret_cast<const u32x2_elem*>(last);
+    raw[0] = u32x4{a[0], a[1], b[0], b[1]};
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store_halves(typename Elem<DT>::type* first, typename Elem<DT>::type* last, const float (&x)[8]) {
+  if constexpr (DT == TF_DT_F32) {
+    store_piece(first, u32x4{f32_to_bits(x[0]), f32_to_bits(x[1]), f32_to_bits(x[2]), f32_to_bits(x[3])});
+    store_piece(last, u32x4{f32_to_bits(x[4]), f32_to_bits(x[5]), f32_to_bits(x[6]), f32_to_bits(x[7])});
+  } else {
+    const u32x4 v = Elem<DT>::pack(x);
+    *reinterpret_cast<u32x2_elem*>(first) = u32x2_elem{v[0], v[1]};
+    *reinterpret_cast<u32x2_elem*>(last) = u32x2_elem{v[2], v[3]};
   }
 }
 
@@ -70,7 +95,9 @@ __device__ __forceinline__ float mean_square(const float (&x)[8], const float (&
   return lanes_join<LANES>(squares, [](float u, float v) { return u + v; }) / (float)dim;
 }
 
-template <int DT, int LANES>
+// SPLIT: rotary_dim is 8 more than a multiple of 16. The last lane that turns has half a piece of either half, and
+// makes its pieces whole with what stands behind rotary_dim.
+template <int DT, int LANES, bool SPLIT>
 __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_norm_rotate_args a, RotatePlan p) {
   typedef typename Elem<DT>::type T;
   __shared__ float cosines[kTurns], sines[kTurns];
@@ -78,9 +105,12 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
   const int here = min(p.tokens, all - first), angles = a.rotary_dim / 2;
   const int u = threadIdx.x % LANES;
   const bool have = u < a.head_dim / 16;  // the others add zeros to the sum
-  const bool turned = u < a.rotary_dim / 16;
+  const bool turned = 16 * u < a.rotary_dim;
+  const bool all_turned = !SPLIT || 16 * u + 8 < a.rotary_dim;  // not only the first halves of its pieces' pairs
   const bool halves = turned && !a.interleaved;
   const int at0 = halves ? 8 * u : 16 * u, at1 = halves ? angles + 8 * u : 16 * u + 8;
+  const bool apart = halves && !all_turned;
+  const int rest0 = apart ? a.rotary_dim : at0 + 4, rest1 = apart ? a.rotary_dim + 4 : at1 + 4;
 
   // Rows in this order: the tokens' queries, then their keys.
   struct Place {
@@ -107,6 +137,15 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
     return x;
   };
   auto load = [&](const Place& x, RawRow<DT>& raw) {
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int n = 0; n < RawRow<DT>::kPieces; ++n) raw.x[n] = raw.y[n] = u32x4(0u);
+      if (have) {
+        load_halves<DT>(x.in + at0, x.in + rest0, raw.x);
+        load_halves<DT>(x.in + at1, x.in + rest1, raw.y);
+      }
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < RawRow<DT>::kPieces; ++n) {
       raw.x[n] = raw.y[n] = u32x4(0u);
@@ -154,8 +193,16 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
 #pragma unroll
         for (int n = 0; n < 8; ++n) w0[n] = w1[n] = 1.f;
         if (w && have) {
-          load_weights(w, a.weight_dtype, at0, w0);
-          load_weights(w, a.weight_dtype, at1, w1);
+          if constexpr (SPLIT) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              w0[n] = load_elem(w, a.weight_dtype, (n < 4 ? at0 : rest0 - 4) + n);
+              w1[n] = load_elem(w, a.weight_dtype, (n < 4 ? at1 : rest1 - 4) + n);
+            }
+          } else {
+            load_weights(w, a.weight_dtype, at0, w0);
+            load_weights(w, a.weight_dtype, at1, w1);
+          }
         }
       }
       float square = mean_square<LANES>(x, y, a.head_dim) + a.eps;
@@ -183,20 +230,27 @@ __global__ __launch_bounds__(kRotateThreads) void norm_rotate_kernel(tf_exl3_nor
         for (int n = 0; n < 4; ++n) {
           const float x1 = x[2 * n], x2 = x[2 * n + 1], y1 = y[2 * n], y2 = y[2 * n + 1];
           x[2 * n] = __builtin_fmaf(x1, c[n], -(x2 * s[n])), x[2 * n + 1] = __builtin_fmaf(x1, s[n], x2 * c[n]);
+          if (!all_turned) continue;
           y[2 * n] = __builtin_fmaf(y1, c[4 + n], -(y2 * s[4 + n]));
           y[2 * n + 1] = __builtin_fmaf(y1, s[4 + n], y2 * c[4 + n]);
         }
       } else {
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
+          if (n >= 4 && !all_turned) continue;
           const float one = x[n], two = y[n];
           x[n] = __builtin_fmaf(one, c[n], -(two * s[n])), y[n] = __builtin_fmaf(one, s[n], two * c[n]);
         }
       }
     }
     if (have) {
-      store8<DT>(now.out + at0, x);
-      store8<DT>(now.out + at1, y);
+      if constexpr (SPLIT) {
+        store_halves<DT>(now.out + at0, now.out + rest0, x);
+        store_halves<DT>(now.out + at1, now.out + rest1, y);
+      } else {
+        store8<DT>(now.out + at0, x);
+        store8<DT>(now.out + at1, y);
+      }
     }
     r = ahead, now = next, raw = raw_next;
   }
@@ -222,8 +276,11 @@ static RotatePlan plan_of(const tf_exl3_norm_rotate_args& a, int slots) {
 template <int DT, int LANES>
 static void launch(const tf_exl3_norm_rotate_args& a, hipStream_t stream) {
   const RotatePlan p = plan_of(a, kRotateThreads / LANES);
-  hipLaunchKernelGGL((norm_rotate_kernel<DT, LANES>), dim3((unsigned)(((int64_t)a.batch * a.tokens + p.tokens - 1) / p.tokens), p.parts),
-                     dim3(kRotateThreads), 0, stream, a, p);
+  const dim3 grid((unsigned)(((int64_t)a.batch * a.tokens + p.tokens - 1) / p.tokens), p.parts), threads(kRotateThreads);
+  if (a.rotary_dim % 16 == 0)
+    hipLaunchKernelGGL((norm_rotate_kernel<DT, LANES, false>), grid, threads, 0, stream, a, p);
+  else
+    hipLaunchKernelGGL((norm_rotate_kernel<DT, LANES, true>), grid, threads, 0, stream, a, p);
 }
 
 template <int DT>

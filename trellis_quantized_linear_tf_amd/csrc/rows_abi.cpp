@@ -81,7 +81,7 @@ int tf_exl3_norm_rotate(const tf_exl3_norm_rotate_args* args, void* stream) {
   if (a->batch < 0 || a->tokens < 0 || (int64_t)a->batch * a->tokens >= (1 << 24)) return TF_E_SIZE;
   if (a->q_heads < 1 || a->kv_heads < 1 || a->q_heads > kMostHeads || a->kv_heads > kMostHeads) return TF_E_SIZE;
   if (a->head_dim < 16 || a->head_dim > 512 || a->head_dim % 16 != 0) return TF_E_SIZE;
-  if (a->rotary_dim < 0 || a->rotary_dim > a->head_dim || a->rotary_dim % 16 != 0) return TF_E_SIZE;
+  if (a->rotary_dim != 0 && (a->rotary_dim < 16 || a->rotary_dim > a->head_dim || a->rotary_dim % 8 != 0)) return TF_E_SIZE;
   if (a->norm && !(a->eps >= 0.f && isfinite(a->eps))) return TF_E_SIZE;
   if (a->positions_stride < 0 || a->positions_stride > kMaxStride) return TF_E_SIZE;
   if (!strides_ok(a->q_stride, 1) || !strides_ok(a->k_stride, 1) || !strides_ok(a->q_out_stride, 1) ||
