@@ -517,8 +517,8 @@ int tf_exl3_norm_rotate(const tf_exl3_norm_rotate_args* a, void* stream);
  *   head_dim  a multiple of 16, up to 256; q_heads a multiple of kv_heads
  *   tokens    rows of q, k, v and out, below 2^30; batch below 2^30
  *   offsets   int32 [batch + 1]
- *   strides   [token, head], multiples of 8 elements, those of k and v over tokens at most 2^23,
- *             pointers 16-byte aligned (out: 4 elements, 8 bytes)
+ *   strides   [token, head], multiples of 8 elements, those over tokens at most 2^23 of k and v and 2^31 of
+ *             q and out; pointers 16-byte aligned (out: 4 elements, 8 bytes)
  */
 typedef struct tf_exl3_prompt_attention_args {
   int dtype, tokens, batch, q_heads, kv_heads, head_dim;
@@ -535,7 +535,7 @@ int tf_exl3_prompt_attention(const tf_exl3_prompt_attention_args* a, void* strea
  * A cache in 4 bits. A row of head_dim numbers x is kept in groups of 32:
  *
  *   x as fp32, NaN as 0, within [-65408, 65408] (so that no value is an infinity of fp16)
- *   m = RN16(min x) (never -0),  s = RN16(RN32((max x - min x) / 15))
+ *   m = RN16(min x) (never -0),  s = RN16(RN32(RN32(max x - min x) / 15))
  *   n[i] = rint(RN32(RN32(x[i] - m) / s)) within 0 .. 15 (ties to even), 0 where s is 0
  *
  * and stands for n * s + m: rounded to the type that is asked for, by way of fp32 in bf16. Its
