@@ -10,11 +10,15 @@
 // per tile of 16, and its weights are where O^T = V^T P^T wants them. Only tiles that some row of a wave does
 // not see as a whole are masked.
 //
-// One prompt of 16384 tokens, 32 heads over 8 of 128, bf16: 2.2 TFLOP in 2.00 ms, 1.10 PFLOP/s, where torch's product of
-// 8192^3 reached 1.21 on the same card: matrix products and vector instructions (150 a wave and 64 keys, 32 of them
-// exponentials) fill it between them. Steps of 32 keys whose weights are made between the products of the next step's
-// scores measured 2.11 ms. 24 prompts of 512 to 2050 tokens, fp16: 560 us, 660 TFLOP/s; a tenth of the products each are
-// the diagonal's and those of tiles with two sequences' rows, the rest starts and the last workgroups.
+// One prompt of 16384 tokens, 32 heads over 8 of 128, bf16: 2.2 TFLOP in 2.00 to 2.07 ms, 1.06 to 1.10 PFLOP/s, where torch's
+// product of 8192^3 reached 1.21 to 1.34 on the same cards. By the counters a wave and 64 keys take 64 matrix products and 221
+// other vector instructions, 32 of them exponentials, which count twice: of a SIMD's 4.1e6 cycles the matrix core is busy for 2.1e6 and
+// other vector instructions for 2.1e6, 0.5e6 of them at the same time. Steps of 32 keys whose weights are made between
+// the products of the next step's scores measured 2.11 ms against 2.00. 24 prompts of 512 to 2050 tokens, fp16: 555 to 580 us,
+// 640 to 660 TFLOP/s (passes under a kernel trace 583 to 628 us); a tenth of the products each are the diagonal's and those of tiles with two
+// sequences' rows, and with their masks a step has 338 other vector instructions; the rest are starts and the last workgroups.
+// 8 such prompts of 2048 tokens, TFLOP/s by columns, and one of 16384: 64 554 and 921, 96 536 and 852 (a quarter of the products
+// are with zeros), 128 700 and 1067, 256 592 and 808 (one row tile a wave: half of the products an operand read).
 #include <math.h>
 
 #include "attention_device.hpp"

@@ -15,10 +15,13 @@
 //
 // 32 sequences of 16 nodes, 32 heads over 8 of 128, 16384 positions, bf16: 677 MB in 241 us (with the join's 11), 2.8
 // TB/s, where the cache in 16 bits takes 393. Vector instructions bound it: 564 a wave and tile of 32 positions x 64
-// rows, 272 of them the making of 8192 numbers (17 a word of 8), and 64 matrix products, at two waves a SIMD; their
-// issue adds up to the measured time. Priority around the products is worth 2%. Measured and not kept: making a
+// rows, 272 of them the making of 8192 numbers (17 a word of 8), and 64 matrix products, at two waves a SIMD. Of its 4.7e5 cycles a
+// SIMD has 3.2e5 of vector instructions and 1.3e5 of products, 0.4e5 of them at the same time: 87% busy. Priority around the products
+// is worth 2%. Measured and not kept: making a
 // number's code ahead between the products 270 us; a chunk order without bank conflicts in the writes of values
 // (12% of the LDS's cycles) the same 238.
+// By columns, 16 nodes and one: 64 162 and 101 us, 96 234 and 143, 128 248 and 154; 256 and 16 sequences 426 and 147: 64 rows
+// of 256 columns are two workgroups of 32 rows, which make the same numbers, each alone on its CU.
 #include "q4_device.hpp"
 #include "tree_plan.hpp"
 
@@ -465,14 +468,20 @@ Shape shape_of(const tf_exl3_tree_attention_args& a) {
   if (dp < 256 && rows > 32 && groups * ((rows + 63) / 64) >= 3200) rt = 4;
   // Workgroups a CU that the line is cut for: what it holds (of 256 columns and two row tiles, 84 KB of shared memory,
   // one), but two where a piece would be a few tiles: beginning and joining it takes as long. Two, three, four, us on the
-  // GPU: 1088 places 17.0 / 15.1 / 15.2, 2056 30.0 / 32.7 / 32.5, 4608 29.1 / 31.6 / 32.6, 6336 in two row tiles 43.7 /
-  // 46.1 / -, 8320 41.1 / 45.9 / 47.1, 12480 45.9 / 44.8 / 44.3, 33024 154 / 150 / 151.
+  // GPU, 8 heads of 128: 1088 places 18.1 / 16.0 / 15.7, 1632 19.2 / 20.0 / 18.2, 1904 21.7 / 21.3 / 21.7, 2176 22.0 / 22.3 / 22.5,
+  // 4608 29.0 / 31.7 / 32.9, 6240 in two row tiles 42.1 / 45.1 / -, 6336 so 41.6 / 46.4 / -, 8448 40.5 / 43.4 / 43.9, 9216 43.4 /
+  // 48.8 / 47.2, 10752 49.5 / 49.7 / 53.4, 12480 65.8 / 68.5 / 63.8, 33024 154 / 150 / 151. In between it costs up to 4% elsewhere: 2 heads, 9216
+  // 42.4 / 40.5 / 42.1; 16 heads 48 / 49 / 46; 1 head 2176 21.9 / 23.0 / 22.8, 9216 38.2 / 37.9 / 38.4. 64 columns: 1088 15.3 / 13.4 / 13.3, 2056
+  // 27.0 / 31.2 / 31.0, 4608 22.9 / 23.8 / 24.3, 8320 29.8 / 31.5 / 32.3, 9216 31.1 / 35.4 / 33.0 (a head's slots behind one another: 22.8 /
+  // 25.3 / 25.3, 20.9 / 22.0 / 22.0, 26.4 / 26.1 / 27.6, 27.5 / 27.6 / 27.2), 12480 50.2 / 50.6 / 46.6, 33024 so 105 / 95 / 93.
   const int64_t places = groups * ((rows + 16 * rt - 1) / (16 * rt));
   int resident = dp == 256 && rt == 2 ? 1 : waves_of(dp, rt);
   if (resident > 2 && places >= 2048 && places < 10240) resident = 2;
   return {dp, rt, 1, 4, kQ4Positions, resident};
 }
 
+// By the table's room, not the lengths, which are on the device: 24 sequences of 100 positions and 16 nodes take 13.5 us with a table of
+// their own size and 28.6 with one for 4096 positions or more, one such sequence 8.5 and 11.2 (12.7 for 32768).
 // The more groups there are, the longer one workgroup may take over one of them before two launches and pieces of
 // equal time take less. Whole against cut, us on the GPU, 8 rows of 128 (32 rows): 8 groups, 3 tiles 9.9 / 11.3 (10.2 /
 // 11.7), 4 tiles 11.3 / 11.4, 5 tiles 12.7 / 11.4 (13.0 / 11.8); 128 groups, 6 tiles 16.9 / 16.1 (19.6 / 23.8), 8 tiles
