@@ -311,7 +311,8 @@ int tf_exl3_calib_stream_read(const void* src, size_t bytes, uint32_t* out, int 
  * summed in fp32; probabilities are rounded to the inputs' type for the second
  * product: half an ulp each, and in fp16, for one below 2^-27 of the row's largest, up to
  * 2^-38 of that largest. Their sum and the output stay in fp32 until the one rounding of
- * the output. A value that no node may see never reaches an output, infinities and NaN
+ * the output; the output's sum is taken with weights of up to 2^8 (fp16 2^15), so bf16 values past about
+ * 2^120 over the number of keys may overflow in it. A value that no node may see never reaches an output, infinities and NaN
  * included. The same call gives the same bits; the order of a row's fp32 sums goes by
  * the batch's lengths, table_pages and nodes.
  *
